@@ -11,9 +11,9 @@ Five operators, each with a plain form (elementary torch operations) and the lib
 
 The 4-bit format: 32 consecutive values of a row share a scale 2^e, one byte e + 127 (255 = NaN), and
 each value is a sign and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6, two to a byte, the first in the low half.
-A row is padded with zeros to 64 values (32 bytes of codes) and to 4 scale bytes. e is the one for which
-the block's largest magnitude lies in [3.5, 7) 2^e, or -127 where it would be below that; values above
-6 2^e become 6 2^e, which is off by less than half the grid's last step.
+A row is padded with zeros to 64 values (32 bytes of codes) and to 16 scale bytes. e is the one for which
+the block's largest magnitude lies in [3.5, 7) 2^e, held to -127 .. 125; values above 6 2^e become 6 2^e,
+which is off by less than half the grid's last step.
 """
 import math
 
@@ -153,7 +153,7 @@ def _packed(values):
     code, e = _quantised(values)
     T, B = e.shape
     code = torch.nn.functional.pad(code.reshape(T, B * 32), (0, (B & 1) * 32))
-    scale = torch.nn.functional.pad((e + 127).to(torch.uint8), (0, -B % 4))
+    scale = torch.nn.functional.pad((e + 127).to(torch.uint8), (0, -B % 16))
     return (code[:, 0::2] | (code[:, 1::2] << 4)).contiguous(), scale.contiguous()
 
 
@@ -193,7 +193,7 @@ def prepare(case, seed):
 def _rows4(T, D):
     """Room for T rows of D values in 4 bits."""
     return (torch.zeros((T, 32 * -(-D // 64)), dtype=torch.uint8, device="cuda"),
-            torch.zeros((T, 4 * -(-D // 128)), dtype=torch.uint8, device="cuda"))
+            torch.zeros((T, 16 * -(-D // 512)), dtype=torch.uint8, device="cuda"))
 
 
 # ------------------------------------------------------------------------------------- plain form
@@ -209,8 +209,8 @@ def _quantised(x):
     top = x.abs().amax(2)
     m, e = torch.frexp(top)                       # top = m 2^e, m in [0.5, 1)
     e = e - 3 + (m >= 0.875).to(e.dtype)
-    e = torch.where(top > 0, e, -127).clamp(min=-127)
-    a = torch.ldexp(x.abs(), -e[:, :, None])      # exact: a power of two, and 7 is never reached
+    e = torch.where(top > 0, e, -127).clamp(-127, 125)
+    a = torch.ldexp(x.abs(), -e[:, :, None])      # exact: a power of two
     step = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0))
     a = torch.minimum(torch.round(a / step) * step, torch.full_like(a, 6.0))
     code = torch.where(a < 2, 2 * a, torch.where(a < 4, a + 2, a / 2 + 4)).to(torch.uint8)
@@ -324,7 +324,7 @@ def _exact_rounded(x):
     e = torch.where(top >= 7 * torch.exp2(e), e + 1, e)
     e = torch.where(top >= 7 * torch.exp2(e), e + 1, e)
     e = torch.where(top < 3.5 * torch.exp2(e), e - 1, e)
-    unit = torch.exp2(torch.where(top > 0, e.clamp(min=-127), -127.0))[:, :, None]
+    unit = torch.exp2(torch.where(top > 0, e.clamp(-127, 125), -127.0))[:, :, None]
     at = torch.tensor(_BORDERS, dtype=torch.float64, device=x.device)
     at[0::2] = torch.nextafter(at[0::2], at[0::2] + 1)                  # a tie there goes down
     level = torch.tensor(LEVELS, dtype=torch.float64, device=x.device)
