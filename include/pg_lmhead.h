@@ -55,7 +55,7 @@ enum {
   PG_ERR_NULL = -1,      /* a required pointer is NULL */
   PG_ERR_SHAPE = -2,     /* T < 0, D < 1, V < 1, or a size beyond the supported range */
   PG_ERR_DTYPE = -3,     /* unknown dtype code */
-  PG_ERR_SOFTCAP = -4,   /* softcap negative or not finite; grad_scale not finite */
+  PG_ERR_SOFTCAP = -4,   /* softcap or eps negative or not finite; grad_scale or lr not finite */
   PG_ERR_WORKSPACE = -5, /* workspace smaller than pg_workspace_bytes() asks for */
   PG_ERR_ALIGN = -6,     /* a pointer is not 16-byte aligned */
   PG_ERR_DEVICE = -7,    /* no HIP device, or the current device is not gfx950 */
@@ -64,7 +64,8 @@ enum {
 };
 
 enum { PG_DTYPE_BF16 = 0, PG_DTYPE_F32 = 1 }; /* dtype of H and E (they share one) */
-enum { PG_OP_FWD = 0, PG_OP_BWD = 1, PG_OP_BPB = 2, PG_OP_FWD_Q8 = 3, PG_OP_FWD_BWD = 4 };
+enum { PG_OP_FWD = 0, PG_OP_BWD = 1, PG_OP_BPB = 2, PG_OP_FWD_Q8 = 3, PG_OP_FWD_BWD = 4,
+       PG_OP_LN_BWD = 5, PG_OP_FWD_MX4 = 6 };
 
 /* Largest supported sizes: T rows up to 2^31 - 256 (each row index fits an int32, and one launch
  * of 512-thread workgroups over 256-row tiles stays within 2^32 - 1 work items), V and D up to
@@ -278,6 +279,89 @@ pg_status pg_window_rows(const int32_t* tokens, int64_t n_tokens, int32_t window
 
 pg_status pg_sgd_step_bf16(float* master, const float* grad, float lr, int64_t n, void* embed_bf16,
                            void* stream);
+
+/*
+ * Layer norm of the model's last hidden states: what makes `hidden` for the head, and what carries
+ * the head's dhidden on into the model.
+ *   forward   mean = sum_d x / D, var = sum_d (x - mean)^2 / D, xh = (x - mean) / sqrt(var + eps),
+ *             y = xh weight + bias
+ *   backward  g = dy weight, dx = (g - sum_d g / D - xh sum_d (g xh) / D) / sqrt(var + eps),
+ *             dweight = sum_t dy xh, dbias = sum_t dy
+ * The statistics and the forward's values are formed in float64, rounded to float32 once and from there
+ * to y's type. The backward takes no saved statistics: it forms them again from x.
+ *   x           [T, D] bf16 or f32 (dtype_x)
+ *   weight      [D] f32, NULL = ones;  bias [D] f32, NULL = zeros
+ *   score_mask  [T] uint8 or NULL; rows it leaves out are not read. The forward does not write their
+ *               output rows (the head does not read them), the backward writes zeros to their dx rows
+ *               and adds nothing to dweight and dbias
+ *   eps         >= 0, finite (PG_ERR_SOFTCAP otherwise); with eps = 0 a row of equal values gives NaN
+ *   y           [T, D] bf16 or f32 (dtype_y)
+ *   dy          [T, D] bf16 or f32 (dtype_dy), such as dhidden of pg_lmhead_ce_bwd (f32)
+ *   dx          [T, D] bf16 or f32 (dtype_dx) out, NULL leaves it out
+ *   dweight, dbias  [D] f32 out, overwritten; either may be NULL. Their sums have a fixed order, so
+ *               that equal calls give equal bits. A NaN or an infinity in a scored row leaves no finite
+ *               value in that row of dx; one in x makes all of dweight NaN, one in dy reaches its column
+ *               of dweight and dbias
+ *   workspace   pg_layernorm_bwd: at least pg_workspace_bytes(PG_OP_LN_BWD, T, D, 1) bytes
+ * Outputs must not overlap inputs. pg_layernorm_fwd_mx4 is pg_layernorm_fwd with float32 y followed by
+ * pg_quantize_mx4, in one pass and bit for bit: the head's 4-bit states straight from the norm.
+ */
+pg_status pg_layernorm_fwd(const void* x, int32_t dtype_x, const float* weight, const float* bias,
+                           const uint8_t* score_mask, int64_t T, int32_t D, float eps, void* y, int32_t dtype_y,
+                           void* stream);
+
+pg_status pg_layernorm_fwd_mx4(const void* x, int32_t dtype_x, const float* weight, const float* bias,
+                               const uint8_t* score_mask, int64_t T, int32_t D, float eps, uint8_t* codes,
+                               uint8_t* scales, void* stream);
+
+pg_status pg_layernorm_bwd(const void* x, int32_t dtype_x, const float* weight, const uint8_t* score_mask,
+                           const void* dy, int32_t dtype_dy, int64_t T, int32_t D, float eps, void* dx,
+                           int32_t dtype_dx, float* dweight, float* dbias, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Rows in microscaled 4-bit floating point, and the head on them: both the hidden states and the tied
+ * embedding in 4 bits, their product on the matrix unit's 4-bit form. (The model is quantised to fit
+ * the artifact: trios issue #19, approach table, "Квантование": INT4/INT8; README leaderboard, QAT and
+ * GPTQ rows. The pages define no format.)
+ *   format      blocks of 32 consecutive values of a row share a scale 2^e, held as the byte e + 127
+ *               (255 = every value of the block is NaN); each value is a 4-bit code, bit 3 the sign and
+ *               bits 0 .. 2 the index of one of 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   codes       [T, pg_mx4_code_bytes(D)] uint8: value 2 i in the low half of byte i, value 2 i + 1 in
+ *               the high half; 32 bytes for each 64 values begun, codes past D are zero
+ *   scales      [T, pg_mx4_scale_bytes(D)] uint8, one byte per block, 16 bytes for each 512 values begun;
+ *               bytes past the last block are zero
+ * pg_quantize_mx4: rows of bf16 or f32 to codes and scales, padding included. e is the one for which the
+ *   block's largest magnitude lies in [3.5, 7) 2^e, held to -127 .. 125 (so that 6 2^e is finite); codes are
+ *   the nearest ones, ties to the even one, magnitudes above 6 2^e become 6 2^e (off by less than half
+ *   the last step, but for magnitudes from 7 2^125 on). A block with a NaN or an infinity becomes a block of NaNs (codes zero). Rows that
+ *   score_mask leaves out are neither read nor written.
+ * pg_dequantize_mx4: the values that codes and scales stand for, as bf16 (which holds each of them exactly)
+ *   or f32 (dtype). With it the 4-bit embedding also serves the input lookup, and
+ *   pg_lmhead_ce_fwd scores bf16 states on a 4-bit embedding.
+ * pg_lmhead_ce_fwd_mx4: pg_lmhead_ce_fwd on the values that (hidden_codes, hidden_scales) [T rows] and
+ *   (embed_codes, embed_scales) [V rows] stand for. Products are exact and summed in float32. A block of
+ *   NaNs in a scored row's states turns that row's nats and lse into NaN, one in the embedding those of
+ *   every row. Any D; the padding has to be zero, as pg_quantize_mx4 writes it. workspace: at
+ *   least pg_workspace_bytes(PG_OP_FWD_MX4, T, D, V) bytes. Other arguments and errors as for
+ *   pg_lmhead_ce_fwd.
+ * pg_mx4_code_bytes, pg_mx4_scale_bytes: bytes of a row of D values (host arithmetic; PG_ERR_SHAPE,
+ *   negative, for D < 1 or beyond the supported range).
+ */
+int64_t pg_mx4_code_bytes(int32_t D);
+
+int64_t pg_mx4_scale_bytes(int32_t D);
+
+pg_status pg_quantize_mx4(const void* x, int32_t dtype, const uint8_t* score_mask, int64_t T, int32_t D,
+                          uint8_t* codes, uint8_t* scales, void* stream);
+
+pg_status pg_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t T, int32_t D, void* out,
+                            int32_t dtype, void* stream);
+
+pg_status pg_lmhead_ce_fwd_mx4(const uint8_t* hidden_codes, const uint8_t* hidden_scales,
+                               const uint8_t* embed_codes, const uint8_t* embed_scales, const int32_t* target,
+                               const uint8_t* score_mask, int64_t T, int32_t D, int32_t V, float softcap,
+                               float* nats, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes an entry point needs for these sizes (0 for invalid sizes). */
 size_t pg_workspace_bytes(int32_t op, int64_t T, int32_t D, int32_t V);

@@ -21,6 +21,7 @@ PG_OK = 0
 PG_DTYPE_BF16 = 0
 PG_DTYPE_F32 = 1
 PG_OP_FWD, PG_OP_BWD, PG_OP_BPB, PG_OP_FWD_Q8, PG_OP_FWD_BWD = 0, 1, 2, 3, 4
+PG_OP_LN_BWD, PG_OP_FWD_MX4 = 5, 6
 STATUS_NAMES = {0: "PG_OK", -1: "PG_ERR_NULL", -2: "PG_ERR_SHAPE", -3: "PG_ERR_DTYPE", -4: "PG_ERR_SOFTCAP",
                 -5: "PG_ERR_WORKSPACE", -6: "PG_ERR_ALIGN", -7: "PG_ERR_DEVICE", -8: "PG_ERR_HIP",
                 -9: "PG_ERR_SCRATCH"}
@@ -29,7 +30,9 @@ STATUS_NAMES = {0: "PG_OK", -1: "PG_ERR_NULL", -2: "PG_ERR_SHAPE", -3: "PG_ERR_D
 EXPORTS = ("pg_lmhead_ce_fwd", "pg_lmhead_ce_fwd_noalloc", "pg_lmhead_ce_bwd", "pg_lmhead_ce_fwd_bwd", "pg_lmhead_ce_fwd_asym", "pg_lmhead_ce_bwd_asym",
            "pg_lmhead_ce_fwd_bwd_asym",
            "pg_quantize_q8", "pg_lmhead_ce_fwd_q8", "pg_bpb_reduce", "pg_bpb_accumulate", "pg_window_count",
-           "pg_window_scored", "pg_window_rows", "pg_sgd_step_bf16", "pg_workspace_bytes", "pg_status_str",
+           "pg_window_scored", "pg_window_rows", "pg_sgd_step_bf16", "pg_layernorm_fwd", "pg_layernorm_fwd_mx4",
+           "pg_layernorm_bwd", "pg_mx4_code_bytes", "pg_mx4_scale_bytes", "pg_quantize_mx4", "pg_dequantize_mx4",
+           "pg_lmhead_ce_fwd_mx4", "pg_workspace_bytes", "pg_status_str",
            "pg_abi_version")
 
 
@@ -82,6 +85,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pg_window_rows.restype = i32
     lib.pg_sgd_step_bf16.argtypes = [vp, vp, f32, i64, vp, vp]
     lib.pg_sgd_step_bf16.restype = i32
+    lib.pg_layernorm_fwd.argtypes = [vp, i32, vp, vp, vp, i64, i32, f32, vp, i32, vp]
+    lib.pg_layernorm_fwd.restype = i32
+    lib.pg_layernorm_fwd_mx4.argtypes = [vp, i32, vp, vp, vp, i64, i32, f32, vp, vp, vp]
+    lib.pg_layernorm_fwd_mx4.restype = i32
+    lib.pg_layernorm_bwd.argtypes = [vp, i32, vp, vp, vp, i32, i64, i32, f32, vp, i32, vp, vp, vp, sz, vp]
+    lib.pg_layernorm_bwd.restype = i32
+    lib.pg_mx4_code_bytes.argtypes = [i32]
+    lib.pg_mx4_code_bytes.restype = i64
+    lib.pg_mx4_scale_bytes.argtypes = [i32]
+    lib.pg_mx4_scale_bytes.restype = i64
+    lib.pg_quantize_mx4.argtypes = [vp, i32, vp, i64, i32, vp, vp, vp]
+    lib.pg_quantize_mx4.restype = i32
+    lib.pg_dequantize_mx4.argtypes = [vp, vp, i64, i32, vp, i32, vp]
+    lib.pg_dequantize_mx4.restype = i32
+    lib.pg_lmhead_ce_fwd_mx4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, f32, vp, vp, vp, sz, vp]
+    lib.pg_lmhead_ce_fwd_mx4.restype = i32
     lib.pg_workspace_bytes.argtypes = [i32, i64, i32, i32]
     lib.pg_workspace_bytes.restype = sz
     lib.pg_status_str.argtypes = [i32]
@@ -409,6 +428,127 @@ def pg_sgd_step_bf16(master: torch.Tensor, grad: torch.Tensor, lr: float, embed:
     a.same_device()
     st = load().pg_sgd_step_bf16(_ptr(master), _ptr(grad), float(lr), n, _ptr(embed), _stream(stream))
     _check(st, "pg_sgd_step_bf16")
+
+
+_FLOATS = _BF16 + (torch.float32,)
+
+
+def _enqueue(entry: str, ref: torch.Tensor, stream, *args) -> None:
+    """The library call on the device that holds the tensors, whichever is current: on `stream`, or
+    on that device's current one."""
+    fn = getattr(load(), entry)
+    if ref.device.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else int(stream)), entry)
+    else:
+        with torch.cuda.device(ref.device):
+            _check(fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else int(stream)), entry)
+
+
+def _norm_inputs(a: _Args, x, weight, bias, score_mask):
+    """x [T, D] bf16 or float32, weight and bias float32 [D] or None, score_mask uint8/bool [T] or None."""
+    T, D = _matrix(a, x, "x", _FLOATS)
+    a(weight, "weight", (torch.float32,), numel=D, optional=True)
+    a(bias, "bias", (torch.float32,), numel=D, optional=True)
+    a(score_mask, "score_mask", _MASK, numel=T, optional=True)
+    return T, D
+
+
+def pg_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor],
+                     score_mask: Optional[torch.Tensor], eps: float, y: torch.Tensor, stream=None) -> None:
+    a = _Args("pg_layernorm_fwd")
+    T, D = _norm_inputs(a, x, weight, bias, score_mask)
+    a(y, "y", _FLOATS, shape=(T, D))
+    a.same_device()
+    _enqueue(a.where, x, stream, _ptr(x), _dtype_code(x), _ptr(weight), _ptr(bias), _ptr(score_mask), T, D,
+             float(eps), _ptr(y), _dtype_code(y))
+
+
+def pg_mx4_code_bytes(D: int) -> int:
+    """Bytes of a row of D values' 4-bit codes."""
+    n = int(load().pg_mx4_code_bytes(int(D)))
+    if n < 0:
+        raise PgError(n, "pg_mx4_code_bytes")
+    return n
+
+
+def pg_mx4_scale_bytes(D: int) -> int:
+    """Bytes of a row of D values' block scales."""
+    n = int(load().pg_mx4_scale_bytes(int(D)))
+    if n < 0:
+        raise PgError(n, "pg_mx4_scale_bytes")
+    return n
+
+
+def _mx4_rows(a: _Args, codes, scales, D: int, T: Optional[int] = None, name: str = ""):
+    """codes [T, 32 ceil(D / 64)] and scales [T, 16 ceil(D / 512)], uint8; returns T."""
+    a(codes, name + "codes", (torch.uint8,))
+    if T is None:
+        T = codes.shape[0] if codes.dim() == 2 else -1
+    a(codes, name + "codes", (torch.uint8,), shape=(T, 32 * -(-D // 64)))
+    a(scales, name + "scales", (torch.uint8,), shape=(T, 16 * -(-D // 512)))
+    return T
+
+
+def pg_layernorm_fwd_mx4(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor],
+                         score_mask: Optional[torch.Tensor], eps: float, codes: torch.Tensor,
+                         scales: torch.Tensor, stream=None) -> None:
+    a = _Args("pg_layernorm_fwd_mx4")
+    T, D = _norm_inputs(a, x, weight, bias, score_mask)
+    _mx4_rows(a, codes, scales, D, T)
+    a.same_device()
+    _enqueue(a.where, x, stream, _ptr(x), _dtype_code(x), _ptr(weight), _ptr(bias), _ptr(score_mask), T, D,
+             float(eps), _ptr(codes), _ptr(scales))
+
+
+def pg_layernorm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], score_mask: Optional[torch.Tensor],
+                     dy: torch.Tensor, eps: float, dx: Optional[torch.Tensor], dweight: Optional[torch.Tensor],
+                     dbias: Optional[torch.Tensor], workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    a = _Args("pg_layernorm_bwd")
+    T, D = _norm_inputs(a, x, weight, None, score_mask)
+    a(dy, "dy", _FLOATS, shape=(T, D))
+    a(dx, "dx", _FLOATS, shape=(T, D), optional=True)
+    a(dweight, "dweight", (torch.float32,), numel=D, optional=True)
+    a(dbias, "dbias", (torch.float32,), numel=D, optional=True)
+    ws = _workspace(a, PG_OP_LN_BWD, T, D, 1, x, workspace)
+    _enqueue(a.where, x, stream, _ptr(x), _dtype_code(x), _ptr(weight), _ptr(score_mask), _ptr(dy), _dtype_code(dy),
+             T, D, float(eps), _ptr(dx), PG_DTYPE_F32 if dx is None else _dtype_code(dx), _ptr(dweight),
+             _ptr(dbias), _ptr(ws), ws.numel())
+
+
+def pg_quantize_mx4(x: torch.Tensor, score_mask: Optional[torch.Tensor], codes: torch.Tensor, scales: torch.Tensor,
+                    stream=None) -> None:
+    a = _Args("pg_quantize_mx4")
+    T, D = _matrix(a, x, "x", _FLOATS)
+    a(score_mask, "score_mask", _MASK, numel=T, optional=True)
+    _mx4_rows(a, codes, scales, D, T)
+    a.same_device()
+    _enqueue(a.where, x, stream, _ptr(x), _dtype_code(x), _ptr(score_mask), T, D, _ptr(codes), _ptr(scales))
+
+
+def pg_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    a = _Args("pg_dequantize_mx4")
+    T, D = _matrix(a, out, "out", _FLOATS)
+    _mx4_rows(a, codes, scales, D, T)
+    a.same_device()
+    _enqueue(a.where, out, stream, _ptr(codes), _ptr(scales), T, D, _ptr(out), _dtype_code(out))
+
+
+def pg_lmhead_ce_fwd_mx4(hidden_codes: torch.Tensor, hidden_scales: torch.Tensor, embed_codes: torch.Tensor,
+                         embed_scales: torch.Tensor, target: torch.Tensor, score_mask: Optional[torch.Tensor],
+                         D: int, softcap: float, nats: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    a = _Args("pg_lmhead_ce_fwd_mx4")
+    D = int(D)
+    T = _mx4_rows(a, hidden_codes, hidden_scales, D, name="hidden_")
+    V = _mx4_rows(a, embed_codes, embed_scales, D, name="embed_")
+    a(target, "target", (torch.int32,), numel=T)
+    a(score_mask, "score_mask", _MASK, numel=T, optional=True)
+    a(nats, "nats", (torch.float32,), numel=T)
+    a(lse, "lse", (torch.float32,), numel=T, optional=True)
+    ws = _workspace(a, PG_OP_FWD_MX4, T, D, V, embed_codes, workspace)
+    _enqueue(a.where, embed_codes, stream, _ptr(hidden_codes), _ptr(hidden_scales), _ptr(embed_codes),
+             _ptr(embed_scales), _ptr(target), _ptr(score_mask), T, D, V, float(softcap), _ptr(nats), _ptr(lse),
+             _ptr(ws), ws.numel())
 
 
 def to_device(inp: dict, device="cuda") -> dict:

@@ -7,6 +7,7 @@
 
 #include "../../include/pg_lmhead.h"
 #include "pg_internal.h"
+#include "pg_mx4.h"
 
 namespace {
 
@@ -107,7 +108,7 @@ const char* pg_status_str(pg_status s) {
     case PG_ERR_NULL: return "a required pointer is NULL";
     case PG_ERR_SHAPE: return "invalid shape (T < 0, D < 1, V < 1 or beyond the supported range)";
     case PG_ERR_DTYPE: return "unknown dtype";
-    case PG_ERR_SOFTCAP: return "softcap negative or not finite, or grad_scale or learning rate not finite";
+    case PG_ERR_SOFTCAP: return "softcap or epsilon negative or not finite, or grad_scale or learning rate not finite";
     case PG_ERR_WORKSPACE: return "workspace smaller than pg_workspace_bytes()";
     case PG_ERR_ALIGN: return "pointer not 16-byte aligned";
     case PG_ERR_DEVICE: return "no HIP device, or the current device is not gfx950";
@@ -131,6 +132,8 @@ size_t pg_workspace_bytes(int32_t op, int64_t T, int32_t D, int32_t V) {
     case PG_OP_FWD_Q8:
       if (D % 8 != 0) return 0;
       return pg::align256((size_t)V * (size_t)D * 2) + pg::fwd_workspace(T, D, V).total;
+    case PG_OP_LN_BWD: return pg::norm_bwd_workspace(T, D).total;
+    case PG_OP_FWD_MX4: return pg::fwd_workspace(T, D, V).total;
     default: return 0;
   }
 }
@@ -432,6 +435,125 @@ pg_status pg_sgd_step_bf16(float* master, const float* grad, float lr, int64_t n
   if ((s = device_check(dev)) != PG_OK) return s;
   hipError_t e = pg::launch_sgd_step(master, grad, lr, n, static_cast<uint16_t*>(embed_bf16),
                                      static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? PG_OK : PG_ERR_HIP;
+}
+
+// ------------------------------------------------------------------------------- layer norm
+
+static bool dtype_ok(int32_t dtype) { return dtype == PG_DTYPE_BF16 || dtype == PG_DTYPE_F32; }
+
+// Arguments that the norm's entry points share (eps is checked as a softcap is: finite, not negative).
+static pg_status norm_args(const void* x, int32_t dtype_x, const float* weight, const float* bias,
+                           const uint8_t* score_mask, int64_t T, int32_t D, float eps, const void* out,
+                           int32_t dtype_out) {
+  pg_status s;
+  if ((s = check_shape(T, D, 1)) != PG_OK) return s;
+  if (T > 0 && (!x || !out)) return PG_ERR_NULL;
+  if (!dtype_ok(dtype_x) || !dtype_ok(dtype_out)) return PG_ERR_DTYPE;
+  if ((s = check_softcap(eps)) != PG_OK) return s;
+  if (misaligned(x) || misaligned(weight) || misaligned(bias) || misaligned(score_mask) || misaligned(out))
+    return PG_ERR_ALIGN;
+  return PG_OK;
+}
+
+pg_status pg_layernorm_fwd(const void* x, int32_t dtype_x, const float* weight, const float* bias,
+                           const uint8_t* score_mask, int64_t T, int32_t D, float eps, void* y, int32_t dtype_y,
+                           void* stream) {
+  pg_status s;
+  if ((s = norm_args(x, dtype_x, weight, bias, score_mask, T, D, eps, y, dtype_y)) != PG_OK) return s;
+  pg::DeviceInfo dev{};
+  if ((s = device_check(dev)) != PG_OK) return s;
+  hipError_t e = pg::launch_norm(x, dtype_x, weight, bias, score_mask, T, D, eps, y, dtype_y, dev,
+                                 static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? PG_OK : PG_ERR_HIP;
+}
+
+pg_status pg_layernorm_fwd_mx4(const void* x, int32_t dtype_x, const float* weight, const float* bias,
+                               const uint8_t* score_mask, int64_t T, int32_t D, float eps, uint8_t* codes,
+                               uint8_t* scales, void* stream) {
+  pg_status s;
+  if ((s = norm_args(x, dtype_x, weight, bias, score_mask, T, D, eps, codes, PG_DTYPE_F32)) != PG_OK) return s;
+  if (T > 0 && !scales) return PG_ERR_NULL;
+  if (misaligned(scales)) return PG_ERR_ALIGN;
+  pg::DeviceInfo dev{};
+  if ((s = device_check(dev)) != PG_OK) return s;
+  hipError_t e = pg::launch_norm_mx4(x, dtype_x, weight, bias, score_mask, T, D, eps, codes, scales, dev,
+                                     static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? PG_OK : PG_ERR_HIP;
+}
+
+pg_status pg_layernorm_bwd(const void* x, int32_t dtype_x, const float* weight, const uint8_t* score_mask,
+                           const void* dy, int32_t dtype_dy, int64_t T, int32_t D, float eps, void* dx,
+                           int32_t dtype_dx, float* dweight, float* dbias, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  pg_status s;
+  if ((s = norm_args(x, dtype_x, weight, nullptr, score_mask, T, D, eps, dy, dtype_dy)) != PG_OK) return s;
+  if (!dtype_ok(dtype_dx)) return PG_ERR_DTYPE;
+  if (!workspace) return PG_ERR_NULL;
+  if (misaligned(dx) || misaligned(dweight) || misaligned(dbias) || misaligned(workspace)) return PG_ERR_ALIGN;
+  if (workspace_bytes < pg_workspace_bytes(PG_OP_LN_BWD, T, D, 1)) return PG_ERR_WORKSPACE;
+  pg::DeviceInfo dev{};
+  if ((s = device_check(dev)) != PG_OK) return s;
+  hipError_t e = pg::launch_norm_bwd(x, dtype_x, weight, score_mask, dy, dtype_dy, T, D, eps, dx, dtype_dx, dweight,
+                                     dbias, static_cast<char*>(workspace), dev, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? PG_OK : PG_ERR_HIP;
+}
+
+// ------------------------------------------------------------------- microscaled 4-bit rows
+
+int64_t pg_mx4_code_bytes(int32_t D) {
+  return check_shape(0, D, 1) == PG_OK ? pg::mx4_code_bytes(D) : (int64_t)PG_ERR_SHAPE;
+}
+
+int64_t pg_mx4_scale_bytes(int32_t D) {
+  return check_shape(0, D, 1) == PG_OK ? pg::mx4_scale_bytes(D) : (int64_t)PG_ERR_SHAPE;
+}
+
+pg_status pg_quantize_mx4(const void* x, int32_t dtype, const uint8_t* score_mask, int64_t T, int32_t D,
+                          uint8_t* codes, uint8_t* scales, void* stream) {
+  pg_status s;
+  if ((s = check_shape(T, D, 1)) != PG_OK) return s;
+  if (T > 0 && (!x || !codes || !scales)) return PG_ERR_NULL;
+  if (!dtype_ok(dtype)) return PG_ERR_DTYPE;
+  if (misaligned(x) || misaligned(score_mask) || misaligned(codes) || misaligned(scales)) return PG_ERR_ALIGN;
+  pg::DeviceInfo dev{};
+  if ((s = device_check(dev)) != PG_OK) return s;
+  hipError_t e = pg::launch_quantize_mx4(x, dtype, score_mask, T, D, codes, scales, dev,
+                                         static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? PG_OK : PG_ERR_HIP;
+}
+
+pg_status pg_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t T, int32_t D, void* out,
+                            int32_t dtype, void* stream) {
+  pg_status s;
+  if ((s = check_shape(T, D, 1)) != PG_OK) return s;
+  if (T > 0 && (!codes || !scales || !out)) return PG_ERR_NULL;
+  if (!dtype_ok(dtype)) return PG_ERR_DTYPE;
+  if (misaligned(codes) || misaligned(scales) || misaligned(out)) return PG_ERR_ALIGN;
+  pg::DeviceInfo dev{};
+  if ((s = device_check(dev)) != PG_OK) return s;
+  hipError_t e = pg::launch_dequantize_mx4(codes, scales, T, D, out, dtype, dev, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? PG_OK : PG_ERR_HIP;
+}
+
+pg_status pg_lmhead_ce_fwd_mx4(const uint8_t* hidden_codes, const uint8_t* hidden_scales,
+                               const uint8_t* embed_codes, const uint8_t* embed_scales, const int32_t* target,
+                               const uint8_t* score_mask, int64_t T, int32_t D, int32_t V, float softcap,
+                               float* nats, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  pg_status s;
+  if ((s = check_shape(T, D, V)) != PG_OK) return s;
+  if (T > 0 && (!hidden_codes || !hidden_scales || !target || !nats)) return PG_ERR_NULL;
+  if (!embed_codes || !embed_scales || !workspace) return PG_ERR_NULL;
+  if ((s = check_softcap(softcap)) != PG_OK) return s;
+  if (misaligned(hidden_codes) || misaligned(hidden_scales) || misaligned(embed_codes) || misaligned(embed_scales) ||
+      misaligned(target) || misaligned(score_mask) || misaligned(nats) || misaligned(lse) || misaligned(workspace))
+    return PG_ERR_ALIGN;
+  if (workspace_bytes < pg_workspace_bytes(PG_OP_FWD_MX4, T, D, V)) return PG_ERR_WORKSPACE;
+  pg::DeviceInfo dev{};
+  if ((s = device_check(dev)) != PG_OK) return s;
+  hipError_t e = pg::launch_fwd_mx4(hidden_codes, hidden_scales, embed_codes, embed_scales, target, score_mask, T, D,
+                                    V, softcap, nats, lse, static_cast<char*>(workspace), dev,
+                                    static_cast<hipStream_t>(stream));
   return e == hipSuccess ? PG_OK : PG_ERR_HIP;
 }
 

@@ -95,6 +95,34 @@ hipError_t launch_window_rows(const int32_t* tokens, int64_t n_tokens, int32_t w
                               hipStream_t st);
 hipError_t launch_sgd_step(float* master, const float* grad, float lr, int64_t n, uint16_t* out, hipStream_t st);
 
+// Layer norm (pg_norm.hip); dtype codes as in the C ABI. The 4-bit output writes codes and scales.
+hipError_t launch_norm(const void* x, int32_t dtype_x, const float* weight, const float* bias, const uint8_t* mask,
+                       int64_t T, int32_t D, float eps, void* y, int32_t dtype_y,
+                       const DeviceInfo& dev, hipStream_t st);
+hipError_t launch_norm_mx4(const void* x, int32_t dtype_x, const float* weight, const float* bias,
+                           const uint8_t* mask, int64_t T, int32_t D, float eps, uint8_t* codes, uint8_t* scales,
+                           const DeviceInfo& dev, hipStream_t st);
+struct NormBwdWorkspace {
+  size_t part;    // f32[blocks, 2, D]: partial sums of the gradients of the gain and the bias
+  size_t stats;   // f64[T, 2]: mean and reciprocal deviation of each row (rows wider than a wave holds)
+  size_t total;
+};
+NormBwdWorkspace norm_bwd_workspace(int64_t T, int32_t D);
+hipError_t launch_norm_bwd(const void* x, int32_t dtype_x, const float* weight, const uint8_t* mask, const void* dy,
+                           int32_t dtype_dy, int64_t T, int32_t D, float eps, void* dx, int32_t dtype_dx,
+                           float* dweight, float* dbias, char* ws, const DeviceInfo& dev, hipStream_t st);
+
+// Microscaled 4-bit rows (pg_mx4.hip) and the head on them (pg_fwd_mx4.hip); the workspace is the
+// forward's.
+hipError_t launch_quantize_mx4(const void* x, int32_t dtype, const uint8_t* mask, int64_t T, int32_t D,
+                               uint8_t* codes, uint8_t* scales, const DeviceInfo& dev, hipStream_t st);
+hipError_t launch_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t T, int32_t D, void* out,
+                                 int32_t dtype, const DeviceInfo& dev, hipStream_t st);
+hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const uint8_t* ecodes,
+                          const uint8_t* escales, const int32_t* target, const uint8_t* mask, int64_t T, int32_t D,
+                          int32_t V, float cap, float* nats, float* lse, char* ws, const DeviceInfo& dev,
+                          hipStream_t st);
+
 // dZ block layout (the backward's workspace). dZ[t][v] is stored in 32 x 32 blocks laid out like
 // the accumulator of v_mfma_f32_32x32x16_bf16: block (bt, bv) holds tokens 32 bt .. 32 bt + 31 and
 // vocabulary rows 32 bv .. 32 bv + 31 as 1024 bf16 at offset (bt * nvb + bv) * 1024, nvb = number
@@ -157,6 +185,13 @@ constexpr int64_t kMaxStrideBlocks = (int64_t)1 << 16;
 inline unsigned stride_blocks(int64_t count, int64_t per_block) {
   const int64_t b = (count + per_block - 1) / per_block;
   return (unsigned)(b < 1 ? 1 : (b > kMaxStrideBlocks ? kMaxStrideBlocks : b));
+}
+
+// The same for kernels whose workgroups keep something over their rows (the gain of a norm): as many
+// workgroups of 256 threads as the chip holds at once.
+inline unsigned resident_blocks(const DeviceInfo& dev, int64_t count, int64_t per_block) {
+  const int64_t b = (count + per_block - 1) / per_block, most = 8 * (int64_t)(dev.cu_count > 0 ? dev.cu_count : 256);
+  return (unsigned)(b < 1 ? 1 : (b > most ? most : b));
 }
 
 }  // namespace pg

@@ -1,0 +1,514 @@
+// Layer norm of the model's last hidden states (the final norm in front of the tied head: README
+// leaderboard and trios issue name the tied head on the model's last states), forward and backward.
+//
+//   forward    mean = sum_d x / D, var = sum_d (x - mean)^2 / D, r = 1 / sqrt(var + eps)
+//              xh = (x - mean) r,  y = xh w + b
+//   backward   g = dy w,  dx = r (g - sum_d g / D - xh sum_d (g xh) / D)
+//              dw = sum_t dy xh,  db = sum_t dy
+//
+// Both move each row once and are bound by HBM: a row is held in registers by the lanes that read it.
+// The statistics and the forward's values are formed in float64, which costs no more issue time than
+// float32 without packed operations (5.1 against 5.7 cycles per operation and wave) and is hidden
+// under the loads: a row with a mean far above its deviation loses nothing, and the float32 value that
+// is stored or quantised is the correctly rounded one but for one value in about 10^8, so the 4-bit
+// form does not depend on the order of a sum.
+// Rows that score_mask leaves out are neither read nor written by the forward; the backward gives them
+// zero gradients.
+#include "pg_internal.h"
+#include "pg_mx4.h"
+#include "pg_rows.h"
+
+namespace pg {
+
+struct Mx4Out {};   // output in 4 bits
+
+struct NormParams {
+  const void* x;
+  const float* weight;   // nullptr: ones
+  const float* bias;     // nullptr: zeros
+  const uint8_t* mask;
+  int64_t T;
+  int32_t D;
+  double eps;
+  void* y;               // float or bf16 rows, or the codes
+  uint8_t* scales;
+};
+
+// The gain and bias of chunk c (ones and zeros where there are none).
+__device__ __forceinline__ void norm_params_chunk(const NormParams& p, int c, float* w, float* b) {
+  if (p.weight) load_chunk(p.weight, c, p.D, w);
+  if (p.bias) load_chunk(p.bias, c, p.D, b);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (!p.weight) w[j] = 1.f;
+    if (!p.bias) b[j] = 0.f;
+  }
+}
+
+// A chunk's values as float32: xh w + b in float64, rounded once.
+__device__ __forceinline__ void norm_chunk(const float* x, const float* w, const float* b, double mean, double r,
+                                           float* v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = (float)__builtin_fma(((double)x[j] - mean) * r, (double)w[j], (double)b[j]);
+}
+
+template <typename TOut>
+__device__ __forceinline__ void norm_store(const NormParams& p, int64_t t, int c, float* v) {
+  if constexpr (std::is_same<TOut, Mx4Out>::value) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (8 * c + j >= p.D) v[j] = 0.f;   // the row's padding is zero whatever its bias
+    mx4_store_chunk(v, c, p.D, static_cast<uint8_t*>(p.y) + t * mx4_code_bytes(p.D),
+                    p.scales + t * mx4_scale_bytes(p.D));
+  } else {
+    store_chunk(static_cast<TOut*>(p.y) + t * p.D, c, p.D, v);
+  }
+}
+
+// Rows up to kRowWaveMax: LPR lanes hold a row, K chunks each, and a wave 64 / LPR rows.
+template <typename TX, typename TOut, int LPR, int K>
+__global__ __launch_bounds__(256) void norm_rows_kernel(NormParams p) {
+  constexpr int RPW = 64 / LPR;
+  const int lane = threadIdx.x & 63, l = lane % LPR;
+  const int64_t first = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * RPW + lane / LPR;
+  float w[K][8], b[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) norm_params_chunk(p, l + k * LPR, w[k], b[k]);
+  for (int64_t t = first; t < p.T; t += (int64_t)gridDim.x * 4 * RPW) {
+    if (p.mask && !p.mask[t]) continue;
+    float x[K][8];
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) load_chunk(static_cast<const TX*>(p.x) + t * p.D, l + k * LPR, p.D, x[k]);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += (double)x[k][j];
+    const double mean = group_sum<LPR>(s) / p.D;
+    s = 0.0;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double d = 8 * (l + k * LPR) + j < p.D ? (double)x[k][j] - mean : 0.0;
+        s = __builtin_fma(d, d, s);
+      }
+    const double r = 1.0 / sqrt(group_sum<LPR>(s) / p.D + p.eps);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float v[8];
+      norm_chunk(x[k], w[k], b[k], mean, r, v);
+      norm_store<TOut>(p, t, l + k * LPR, v);
+    }
+  }
+}
+
+// Wider rows: a workgroup per row, which reads it three times (from L2 after the first).
+template <typename TX, typename TOut>
+__global__ __launch_bounds__(kRowThreads) void norm_wide_kernel(NormParams p) {
+  __shared__ double sh[kRowThreads / 64];
+  const int nch = (p.D + 127) / 128 * 16;   // chunks, whole runs of 16 lanes
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+    if (p.mask && !p.mask[t]) continue;
+    const TX* row = static_cast<const TX*>(p.x) + t * p.D;
+    float x[8];
+    double s = 0.0;
+    for (int c = threadIdx.x; c < nch; c += kRowThreads) {
+      load_chunk(row, c, p.D, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += (double)x[j];
+    }
+    const double mean = workgroup_sum(s, sh) / p.D;
+    s = 0.0;
+    for (int c = threadIdx.x; c < nch; c += kRowThreads) {
+      load_chunk(row, c, p.D, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double d = 8 * c + j < p.D ? (double)x[j] - mean : 0.0;
+        s = __builtin_fma(d, d, s);
+      }
+    }
+    const double r = 1.0 / sqrt(workgroup_sum(s, sh) / p.D + p.eps);
+    for (int c = threadIdx.x; c < nch; c += kRowThreads) {
+      float v[8], w[8], b[8];
+      load_chunk(row, c, p.D, x);
+      norm_params_chunk(p, c, w, b);
+      norm_chunk(x, w, b, mean, r, v);
+      norm_store<TOut>(p, t, c, v);
+    }
+  }
+}
+
+template <typename TX, typename TOut>
+static void launch_norm_t(const NormParams& p, const DeviceInfo& dev, hipStream_t st) {
+  const int D = p.D;
+  if (D > kRowWaveMax) {
+    hipLaunchKernelGGL((norm_wide_kernel<TX, TOut>), dim3(stride_blocks(p.T, 1)), dim3(kRowThreads), 0, st, p);
+    return;
+  }
+#define PG_NORM(LPR, K)                                                                                          \
+  hipLaunchKernelGGL((norm_rows_kernel<TX, TOut, LPR, K>), dim3(resident_blocks(dev, p.T, 4 * (64 / LPR))),     \
+                     dim3(256), 0, st, p)
+  if (D <= 128) PG_NORM(16, 1);
+  else if (D <= 256) PG_NORM(32, 1);
+  else if (D <= 512) PG_NORM(64, 1);
+  else if (D <= 1024) PG_NORM(64, 2);
+  else PG_NORM(64, 4);
+#undef PG_NORM
+}
+
+static NormParams norm_params(const void* x, const float* weight, const float* bias, const uint8_t* mask, int64_t T,
+                              int32_t D, float eps, void* y, uint8_t* scales) {
+  NormParams p{};
+  p.x = x;
+  p.weight = weight;
+  p.bias = bias;
+  p.mask = mask;
+  p.T = T;
+  p.D = D;
+  p.eps = (double)eps;
+  p.y = y;
+  p.scales = scales;
+  return p;
+}
+
+hipError_t launch_norm(const void* x, int32_t dtype_x, const float* weight, const float* bias, const uint8_t* mask,
+                       int64_t T, int32_t D, float eps, void* y, int32_t dtype_y,
+                       const DeviceInfo& dev, hipStream_t st) {
+  if (T == 0) return hipSuccess;
+  const NormParams p = norm_params(x, weight, bias, mask, T, D, eps, y, nullptr);
+  if (dtype_x == 0) {
+    if (dtype_y == 0) launch_norm_t<uint16_t, uint16_t>(p, dev, st);
+    else launch_norm_t<uint16_t, float>(p, dev, st);
+  } else {
+    if (dtype_y == 0) launch_norm_t<float, uint16_t>(p, dev, st);
+    else launch_norm_t<float, float>(p, dev, st);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_mx4(const void* x, int32_t dtype_x, const float* weight, const float* bias,
+                           const uint8_t* mask, int64_t T, int32_t D, float eps, uint8_t* codes, uint8_t* scales,
+                           const DeviceInfo& dev, hipStream_t st) {
+  if (T == 0) return hipSuccess;
+  const NormParams p = norm_params(x, weight, bias, mask, T, D, eps, codes, scales);
+  if (dtype_x == 0) launch_norm_t<uint16_t, Mx4Out>(p, dev, st);
+  else launch_norm_t<float, Mx4Out>(p, dev, st);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------------- backward
+
+struct NormBwdParams {
+  const void* x;
+  const void* dy;
+  const float* weight;
+  const uint8_t* mask;
+  int64_t T;
+  int32_t D;
+  double eps;
+  void* dx;       // nullptr: not wanted
+  float* part;    // partial sums of dw and db per workgroup [blocks][2][D]; nullptr: not wanted
+  double* stats;  // wide rows: mean and r of each row, for the column sums
+};
+
+// Rows up to kRowWaveMax. Each lane keeps the sums of dw and db over its rows for its own columns; at
+// the end the waves of a workgroup add theirs in wave order through LDS, so that the result does not
+// depend on timing.
+template <typename TX, typename TDY, typename TDX, int LPR, int K>
+__global__ __launch_bounds__(256) void norm_bwd_rows_kernel(NormBwdParams p) {
+  constexpr int RPW = 64 / LPR;
+  __shared__ float sums[2][LPR * K * 8];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % LPR;
+  float w[K][8], dw[K][8], db[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (p.weight) load_chunk(p.weight, l + k * LPR, p.D, w[k]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!p.weight) w[k][j] = 1.f;
+      dw[k][j] = db[k][j] = 0.f;
+    }
+  }
+  const float invD = 1.0f / (float)p.D;
+  const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * RPW + lane / LPR;
+  for (int64_t t = first; t < p.T; t += (int64_t)gridDim.x * 4 * RPW) {
+    TDX* dxrow = static_cast<TDX*>(p.dx) + t * p.D;
+    if (p.mask && !p.mask[t]) {
+      if (p.dx) {
+        const float zero[8] = {};
+#pragma unroll
+        for (int k = 0; k < K; ++k) store_chunk(dxrow, l + k * LPR, p.D, zero);
+      }
+      continue;
+    }
+    float x[K][8], dy[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      load_chunk(static_cast<const TX*>(p.x) + t * p.D, l + k * LPR, p.D, x[k]);
+      load_chunk(static_cast<const TDY*>(p.dy) + t * p.D, l + k * LPR, p.D, dy[k]);
+    }
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += (double)x[k][j];
+    const double mean = group_sum<LPR>(s) / p.D;
+    s = 0.0;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double d = 8 * (l + k * LPR) + j < p.D ? (double)x[k][j] - mean : 0.0;
+        x[k][j] = (float)d;
+        s = __builtin_fma(d, d, s);
+      }
+    const float r = (float)(1.0 / sqrt(group_sum<LPR>(s) / p.D + p.eps));
+    float c1 = 0.f, c2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xh = x[k][j] * r, g = dy[k][j] * w[k][j];
+        x[k][j] = xh;
+        c1 += g;
+        c2 = __builtin_fmaf(g, xh, c2);
+        dw[k][j] = __builtin_fmaf(dy[k][j], xh, dw[k][j]);
+        db[k][j] += dy[k][j];
+      }
+    c1 = group_sum<LPR>(c1) * invD;
+    c2 = group_sum<LPR>(c2) * invD;
+    if (p.dx) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = r * (__builtin_fmaf(dy[k][j], w[k][j], -c1) - x[k][j] * c2);
+        store_chunk(dxrow, l + k * LPR, p.D, v);
+      }
+    }
+  }
+  if (!p.part) return;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {   // the rows that the wave's groups hold side by side
+#pragma unroll
+      for (int off = LPR; off < 64; off <<= 1) {
+        dw[k][j] += __shfl_xor(dw[k][j], off);
+        db[k][j] += __shfl_xor(db[k][j], off);
+      }
+    }
+  for (int q = 0; q < 4; ++q) {
+    if (wave == q && lane < LPR) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float* a = &sums[0][(l + k * LPR) * 8 + j];
+          float* b = &sums[1][(l + k * LPR) * 8 + j];
+          *a = q ? *a + dw[k][j] : dw[k][j];
+          *b = q ? *b + db[k][j] : db[k][j];
+        }
+    }
+    __syncthreads();
+  }
+  float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
+  for (int d = threadIdx.x; d < p.D; d += 256) {
+    part[d] = sums[0][d];
+    part[p.D + d] = sums[1][d];
+  }
+}
+
+// Wider rows: dx by a workgroup per row, the row's statistics kept for the column sums.
+template <typename TX, typename TDY, typename TDX>
+__global__ __launch_bounds__(kRowThreads) void norm_bwd_wide_kernel(NormBwdParams p) {
+  __shared__ double sh[kRowThreads / 64];
+  const int nch = (p.D + 7) / 8;
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+    TDX* dxrow = static_cast<TDX*>(p.dx) + t * p.D;
+    if (p.mask && !p.mask[t]) {
+      const float zero[8] = {};
+      if (p.dx)
+        for (int c = threadIdx.x; c < nch; c += kRowThreads) store_chunk(dxrow, c, p.D, zero);
+      continue;
+    }
+    const TX* row = static_cast<const TX*>(p.x) + t * p.D;
+    const TDY* dyrow = static_cast<const TDY*>(p.dy) + t * p.D;
+    float x[8], dy[8], w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 1.f;
+    double s = 0.0;
+    for (int c = threadIdx.x; c < nch; c += kRowThreads) {
+      load_chunk(row, c, p.D, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += (double)x[j];
+    }
+    const double mean = workgroup_sum(s, sh) / p.D;
+    double c1 = 0.0, c2 = 0.0;
+    s = 0.0;
+    for (int c = threadIdx.x; c < nch; c += kRowThreads) {
+      load_chunk(row, c, p.D, x);
+      load_chunk(dyrow, c, p.D, dy);
+      if (p.weight) load_chunk(p.weight, c, p.D, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double d = 8 * c + j < p.D ? (double)x[j] - mean : 0.0;
+        const double g = (double)dy[j] * (double)w[j];
+        s = __builtin_fma(d, d, s);
+        c1 += g;
+        c2 = __builtin_fma(g, d, c2);
+      }
+    }
+    const double r = 1.0 / sqrt(workgroup_sum(s, sh) / p.D + p.eps);
+    c1 = workgroup_sum(c1, sh) / p.D;
+    c2 = workgroup_sum(c2, sh) * r / p.D;
+    if (p.stats && threadIdx.x == 0) {
+      p.stats[2 * t] = mean;
+      p.stats[2 * t + 1] = r;
+    }
+    if (!p.dx) continue;
+    for (int c = threadIdx.x; c < nch; c += kRowThreads) {
+      float v[8];
+      load_chunk(row, c, p.D, x);
+      load_chunk(dyrow, c, p.D, dy);
+      if (p.weight) load_chunk(p.weight, c, p.D, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = (float)(r * ((double)dy[j] * (double)w[j] - c1 - ((double)x[j] - mean) * r * c2));
+      store_chunk(dxrow, c, p.D, v);
+    }
+  }
+}
+
+// Column sums of wide rows: thread = eight columns, workgroup (x, y) = a run of columns of every
+// gridDim.y-th row from y on.
+template <typename TX, typename TDY>
+__global__ __launch_bounds__(kRowThreads) void norm_bwd_columns_kernel(NormBwdParams p) {
+  const int c = blockIdx.x * kRowThreads + threadIdx.x;
+  if (8 * (int64_t)c >= p.D) return;
+  double dw[8] = {}, db[8] = {};
+  for (int64_t t = blockIdx.y; t < p.T; t += gridDim.y) {
+    if (p.mask && !p.mask[t]) continue;
+    float x[8], dy[8];
+    load_chunk(static_cast<const TX*>(p.x) + t * p.D, c, p.D, x);
+    load_chunk(static_cast<const TDY*>(p.dy) + t * p.D, c, p.D, dy);
+    const double mean = p.stats[2 * t], r = p.stats[2 * t + 1];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      dw[j] = __builtin_fma((double)dy[j], ((double)x[j] - mean) * r, dw[j]);
+      db[j] += (double)dy[j];
+    }
+  }
+  float* part = p.part + (int64_t)blockIdx.y * 2 * p.D;
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = (float)dw[j];
+  store_chunk(part, c, p.D, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = (float)db[j];
+  store_chunk(part + p.D, c, p.D, v);
+}
+
+// dw and db from the partial sums, in block order in float64: wave w of a workgroup takes every 16th
+// block from w on for 64 columns, and the waves' sums are added in wave order.
+constexpr int kNormSumThreads = 1024;
+__global__ __launch_bounds__(kNormSumThreads) void norm_bwd_sum_kernel(const float* part, int blocks, int D, float* dw,
+                                                                       float* db) {
+  __shared__ double sh[kNormSumThreads / 64][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t i = (int64_t)blockIdx.x * 64 + lane, n = 2 * (int64_t)D;
+  double s = 0.0;
+  if (i < n)
+    for (int b = wave; b < blocks; b += kNormSumThreads / 64) s += (double)part[b * n + i];
+  sh[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && i < n) {
+    for (int w = 1; w < kNormSumThreads / 64; ++w) s += sh[w][lane];
+    if (i < D) {
+      if (dw) dw[i] = (float)s;
+    } else if (db) {
+      db[i - D] = (float)s;
+    }
+  }
+}
+
+constexpr int kNormBwdBlocks = 512;     // workgroups of the backward, and partial sums
+constexpr int kNormColumnRows = 64;     // rows of T that split the column sums of wide rows, at most
+
+NormBwdWorkspace norm_bwd_workspace(int64_t T, int32_t D) {
+  NormBwdWorkspace L;
+  const bool wide = D > kRowWaveMax;
+  L.part = 0;
+  L.stats = align256((size_t)(wide ? kNormColumnRows : kNormBwdBlocks) * 2 * (size_t)D * 4);
+  L.total = L.stats + (wide ? align256((size_t)T * 16) : 0);
+  return L;
+}
+
+template <typename TX, typename TDY, typename TDX>
+static void launch_norm_bwd_t(const NormBwdParams& p, int& blocks, hipStream_t st) {
+  const int D = p.D;
+  if (D > kRowWaveMax) {
+    hipLaunchKernelGGL((norm_bwd_wide_kernel<TX, TDY, TDX>), dim3(stride_blocks(p.T, 1)), dim3(kRowThreads), 0, st, p);
+    if (p.part) {
+      blocks = (int)(p.T < kNormColumnRows ? p.T : kNormColumnRows);
+      hipLaunchKernelGGL((norm_bwd_columns_kernel<TX, TDY>), dim3((D + 8 * kRowThreads - 1) / (8 * kRowThreads), blocks),
+                         dim3(kRowThreads), 0, st, p);
+    }
+    return;
+  }
+#define PG_NORM_BWD(LPR, K)                                                                                      \
+  {                                                                                                              \
+    const int64_t need = (p.T + 4 * (64 / LPR) - 1) / (4 * (64 / LPR));                                           \
+    blocks = (int)(need < kNormBwdBlocks ? need : kNormBwdBlocks);                                                \
+    hipLaunchKernelGGL((norm_bwd_rows_kernel<TX, TDY, TDX, LPR, K>), dim3(blocks), dim3(256), 0, st, p);         \
+  }
+  if (D <= 128) PG_NORM_BWD(16, 1)
+  else if (D <= 256) PG_NORM_BWD(32, 1)
+  else if (D <= 512) PG_NORM_BWD(64, 1)
+  else if (D <= 1024) PG_NORM_BWD(64, 2)
+  else PG_NORM_BWD(64, 4)
+#undef PG_NORM_BWD
+}
+
+hipError_t launch_norm_bwd(const void* x, int32_t dtype_x, const float* weight, const uint8_t* mask, const void* dy,
+                           int32_t dtype_dy, int64_t T, int32_t D, float eps, void* dx, int32_t dtype_dx,
+                           float* dweight, float* dbias, char* ws, const DeviceInfo& dev, hipStream_t st) {
+  const NormBwdWorkspace L = norm_bwd_workspace(T, D);
+  NormBwdParams p{};
+  p.x = x;
+  p.dy = dy;
+  p.weight = weight;
+  p.mask = mask;
+  p.T = T;
+  p.D = D;
+  p.eps = (double)eps;
+  p.dx = dx;
+  if (dweight || dbias) {
+    p.part = reinterpret_cast<float*>(ws + L.part);
+    p.stats = reinterpret_cast<double*>(ws + L.stats);
+  }
+  int blocks = 0;
+  if (T > 0) {
+    const int code = dtype_x * 4 + dtype_dy * 2 + dtype_dx;
+    switch (code) {
+      case 0: launch_norm_bwd_t<uint16_t, uint16_t, uint16_t>(p, blocks, st); break;
+      case 1: launch_norm_bwd_t<uint16_t, uint16_t, float>(p, blocks, st); break;
+      case 2: launch_norm_bwd_t<uint16_t, float, uint16_t>(p, blocks, st); break;
+      case 3: launch_norm_bwd_t<uint16_t, float, float>(p, blocks, st); break;
+      case 4: launch_norm_bwd_t<float, uint16_t, uint16_t>(p, blocks, st); break;
+      case 5: launch_norm_bwd_t<float, uint16_t, float>(p, blocks, st); break;
+      case 6: launch_norm_bwd_t<float, float, uint16_t>(p, blocks, st); break;
+      default: launch_norm_bwd_t<float, float, float>(p, blocks, st); break;
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (!p.part) return hipSuccess;
+  // no rows: the sums of nothing
+  hipLaunchKernelGGL(norm_bwd_sum_kernel, dim3((unsigned)((2 * (int64_t)D + 63) / 64)), dim3(kNormSumThreads), 0, st,
+                     p.part, blocks, D, dweight, dbias);
+  return hipGetLastError();
+}
+
+}  // namespace pg

@@ -22,6 +22,12 @@ What it computes, and where the pages state it:
   symmetric int8 with float32
   scales is the reading taken, and the head computes on the bfloat16 rounding of q * scale
   (quantize_rows_q8, dequantize_rows_q8, forward_q8).
+* Quantised head in 4 bits: the same rows name INT4; the reading taken is microscaled 4-bit floating
+  point, blocks of 32 values of a row with a shared power-of-two scale and the magnitudes 0, 0.5, 1,
+  1.5, 2, 3, 4, 6 (quantize_rows_mx4 gives the values that codes and scales stand for); the head
+  computes on the quantised states and embedding.
+* Layer norm of the last hidden states in front of the head, and its backward (layer_norm,
+  layer_norm_backward): biased variance, eps inside the root.
 * Cross-entropy against the next token, in nats: lse(s) - s[target] (trios issue, "Контекст":
   cross-entropy loss and bits per byte; repo-explainer, baseline listing: the loss of the logits against
   the next tokens).
@@ -58,7 +64,7 @@ LN2 = float(np.log(2.0))
 
 __all__ = ["LN2", "logits", "softcap", "softcap_derivative", "log_sum_exp", "forward", "bpb",
            "backward", "embed_grad_rows", "loss", "quantize_rows_q8", "dequantize_rows_q8", "forward_q8",
-           "window_schedule", "sliding_window_eval"]
+           "quantize_rows_mx4", "layer_norm", "layer_norm_backward", "window_schedule", "sliding_window_eval"]
 
 
 def logits(H: np.ndarray, E: np.ndarray) -> np.ndarray:
@@ -202,6 +208,63 @@ def dequantize_rows_q8(q, scale) -> np.ndarray:
 def forward_q8(H, q, scale, target, c, mask=None):
     """Forward of the quantised tied head: :func:`forward` on the dequantised embedding."""
     return forward(H, dequantize_rows_q8(q, scale), target, c, mask)
+
+
+MX4_LEVELS = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def quantize_rows_mx4(x):
+    """(values, codes, exponents) of rows [T, D] in 4 bits: codes [T, D] (bit 3 the sign, bits 0 .. 2 the
+    level), exponents [T, ceil(D / 32)]. Block by block: the exponent is the smallest e with
+    max |x| < 7 2^e, held to -127 .. 125 (6 2^125 is finite in float32), the code the nearest level, ties to the even code, at most 6. A block with a NaN
+    or an infinity becomes NaNs (codes 0, exponent 128)."""
+    x = np.asarray(x, dtype=np.float64)
+    T, D = x.shape
+    values, codes = np.zeros((T, D)), np.zeros((T, D), dtype=np.uint8)
+    exps = np.zeros((T, -(-D // 32)), dtype=np.int64)
+    for b in range(exps.shape[1]):
+        v = x[:, 32 * b:32 * b + 32]
+        top = np.max(np.abs(v), axis=1)
+        bad = ~np.isfinite(top)
+        e = np.full(T, -127, dtype=np.int64)
+        for i in np.nonzero(~bad & (top > 0))[0]:
+            k = int(np.floor(np.log2(top[i]))) - 4      # far enough down, then up to the first that fits
+            while top[i] >= 7 * 2.0 ** k:
+                k += 1
+            e[i] = min(max(k, -127), 125)
+        a = np.abs(v) / np.exp2(e.astype(np.float64))[:, None]
+        # the nearest level; of two equally near ones that with the even code (these are looked at first)
+        order = np.array([0, 2, 4, 6, 1, 3, 5, 7])
+        best = order[np.argmin(np.abs(np.where(np.isfinite(a), a, 0.0)[:, :, None] - MX4_LEVELS[order]), axis=2)]
+        code = best.astype(np.uint8) | (np.signbit(v).astype(np.uint8) << 3)
+        val = np.where(np.signbit(v), -1.0, 1.0) * MX4_LEVELS[best] * np.exp2(e.astype(np.float64))[:, None]
+        code[bad], val[bad], e[bad] = 0, np.nan, 128
+        values[:, 32 * b:32 * b + 32], codes[:, 32 * b:32 * b + 32], exps[:, b] = val, code, e
+    return values, codes, exps
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
+    """y = (x - mean) / sqrt(var + eps) * weight + bias over the rows of x [T, D]."""
+    x = np.asarray(x, dtype=np.float64)
+    d = x - np.mean(x, axis=1, keepdims=True)
+    y = d / np.sqrt(np.mean(d * d, axis=1, keepdims=True) + eps)
+    if weight is not None:
+        y = y * np.asarray(weight, dtype=np.float64)
+    return y if bias is None else y + np.asarray(bias, dtype=np.float64)
+
+
+def layer_norm_backward(x, weight, dy, eps: float = 1e-5, mask=None):
+    """(dx, dweight, dbias) of sum(dy * layer_norm(x)) over the scored rows."""
+    x, dy = np.asarray(x, dtype=np.float64), np.asarray(dy, dtype=np.float64)
+    T, D = x.shape
+    on = _scored(T, mask)
+    w = np.ones(D) if weight is None else np.asarray(weight, dtype=np.float64)
+    d = x - np.mean(x, axis=1, keepdims=True)
+    r = 1.0 / np.sqrt(np.mean(d * d, axis=1, keepdims=True) + eps)
+    xh, g = d * r, dy * w
+    dx = r * (g - np.mean(g, axis=1, keepdims=True) - xh * np.mean(g * xh, axis=1, keepdims=True))
+    dx[~on] = 0.0
+    return dx, np.sum((dy * xh)[on], axis=0), np.sum(dy[on], axis=0)
 
 
 def loss(H, E, target, c: float, g: float, mask=None) -> float:
