@@ -43,6 +43,13 @@ __host__ __device__ __forceinline__ int mx4_splits(int64_t n, int nblocks, int g
   return s < 1 ? 1 : (s > nblocks ? nblocks : (int)s);
 }
 
+// The target's term is one of the sum's, so a negative difference is a rounding (NaN passes).
+__device__ __forceinline__ float not_below_zero(float d) { return d < 0.f ? 0.f : d; }
+
+// The partial sums of a row's splits lie side by side, from a 16-byte boundary where there are several
+// (so that n rows of S splits take at most twice n S entries).
+__host__ __device__ __forceinline__ int mx4_split_stride(int S) { return S <= 2 ? S : (S + 3) & ~3; }
+
 __device__ __forceinline__ f32x16 mfma_mx4(const i32x4& a, int sa, const i32x4& b, int sb, const f32x16& c) {
   const i32x8 aa = {a[0], a[1], a[2], a[3]}, bb = {b[0], b[1], b[2], b[3]};
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(aa, bb, c, 4, 4, 0, sa, 0, sb);
@@ -102,8 +109,9 @@ __global__ __launch_bounds__(256) void fwd_mx4_stream_kernel(FwdMx4Params p) {
   const float sy2 = __shfl_xor(sy, 32);
   const bool here = y >= b0 * 32 && y < b1 * 32 && y < p.V;   // this split holds the target's row
   if (h == 0 && tok < n) {
-    p.part_l[(int64_t)split * n + tok] = l;
-    p.part_m[(int64_t)split * n + tok] = m;
+    const int64_t at = tok * mx4_split_stride(S) + split;
+    p.part_l[at] = l;
+    p.part_m[at] = m;
     if (here) p.s_target[tok] = ((y >> 2) & 1) ? sy2 : sy;
     else if (split == 0 && !(y >= 0 && y < p.V)) p.s_target[tok] = __builtin_nanf("");
   }
@@ -149,6 +157,20 @@ __device__ __forceinline__ void lds_dma16_base(const uint8_t* base, uint32_t off
       : "memory");
 }
 
+// The same with 4 bytes per lane, to 256 bytes of LDS.
+__device__ __forceinline__ void lds_dma4_base(const uint8_t* base, uint32_t offset, uint32_t lds_addr) {
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %3\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, %2\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(offset), "s"(base), "s"(lds_addr)
+      : "memory");
+}
+
 // The scale bytes of a lane's half of each step: of 16 bytes (blocks 0 .. 15) bytes h, h + 2, ...: byte j
 // of word i belongs to step 4 i + j.
 template <int NW>
@@ -165,19 +187,26 @@ __device__ __forceinline__ f32x16 mfma_mx4_op(const i32x4& a, int sa, const i32x
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(aa, bb, c, 4, 4, OP, sa, OP, sb);
 }
 
-// acc = the 32 x 32 logits of fragments a against the rows hf, step after step.
-template <int KS, int NW, int K = 0>
-__device__ __forceinline__ void mx4_chain(const i32x4 (&a)[KS], const int (&sa)[NW], const i32x4 (&hf)[KS],
-                                          const int (&hs)[NW], f32x16& acc) {
-  if constexpr (K < KS) {
-    acc = mfma_mx4_op<K & 3>(a[K], sa[K >> 2], hf[K], hs[K >> 2], acc);
-    mx4_chain<KS, NW, K + 1>(a, sa, hf, hs, acc);
+// Step k of a chain (an unrolled loop's k is a constant, which the switch folds on): words of four steps'
+// scales, byte k % 4.
+__device__ __forceinline__ f32x16 mx4_step(int k, const i32x4& a, const int* sa, const i32x4& b, const int* sb,
+                                           const f32x16& acc) {
+  switch (k & 3) {
+    case 0: return mfma_mx4_op<0>(a, sa[k >> 2], b, sb[k >> 2], acc);
+    case 1: return mfma_mx4_op<1>(a, sa[k >> 2], b, sb[k >> 2], acc);
+    case 2: return mfma_mx4_op<2>(a, sa[k >> 2], b, sb[k >> 2], acc);
+    default: return mfma_mx4_op<3>(a, sa[k >> 2], b, sb[k >> 2], acc);
   }
 }
 
-template <int KS, bool FIXED>
+// Forms of the sum: a softcap in the fixed-shift range, no softcap, a larger softcap (the last two with a
+// reference that follows the largest logit).
+enum Mx4Form { kMx4Fixed, kMx4Uncapped, kMx4Capped };
+
+template <int KS, Mx4Form FORM>
 __global__ __launch_bounds__(512, KS <= 8 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Params p) {
   using TL = Mx4Tile<KS>;
+  constexpr bool FIXED = FORM == kMx4Fixed;
   constexpr int NW = (KS + 3) / 4;          // words of a lane's scales
   constexpr int NS = TL::kScaleBytes / 16;
   __shared__ __attribute__((aligned(1024))) char smem[2 * TL::kBytes];
@@ -195,36 +224,43 @@ __global__ __launch_bounds__(512, KS <= 8 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Par
   const int per = (ntiles + S - 1) / S;
   const int t0 = split * per, t1 = min(t0 + per, ntiles);
 
-  // this wave's part of a tile: kLoads pieces of codes (piece j: 1 KiB, lane i its 16 bytes at 16 i),
-  // and of the scales, which the first waves copy
-  constexpr int RPI = 1024 / TL::kRowBytes;   // rows of a piece
-  const int prow = lane / TL::CPR;            // row in a piece; swizzle(row) is the same for all of a wave's pieces
-  int lchunk = (lane % TL::CPR) ^ TL::swizzle(wave * RPI + prow);
+  // This wave's part of a tile: kLoads pieces of codes (piece j: 1 KiB, lane i its 16 bytes at 16 i), and
+  // a 256-byte piece of the scales. A lane's offset in a piece is the same for each.
+  constexpr int RPI = 1024 / TL::kRowBytes;                 // rows of a piece
+  constexpr int SPR = TL::kScaleBytes / 4, SRPI = 64 / SPR; // words of a row of scales, rows of a piece
+  static_assert(TL::kRows * TL::kScaleBytes == 8 * 256, "a piece of scales per wave");
+  const int prow = lane / TL::CPR, srow = lane / SPR;
+  int lchunk = (lane % TL::CPR) ^ TL::swizzle(wave * RPI + prow);   // the same for all pieces of the wave
   if (lchunk >= 2 * p.steps) lchunk = 0;      // not in the rows (read by no one, or against zero states)
-  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-  constexpr int kScaleLoads = TL::kRows * TL::kScaleBytes / 1024;   // 1 KiB pieces of scales
-  constexpr int SPR = TL::kScaleBytes / 16, SRPI = 64 / SPR;        // 16-byte parts of a row, rows of a piece
   int spart = lane % SPR;
-  if (16 * spart >= p.sb) spart = 0;
-  auto load_tile = [&](int tile, int buf) {
-    const int v0 = tile * TL::kRows;
-    const uint32_t dst = lds0 + buf * TL::kBytes;
-    const uint8_t* cbase = p.ec + (int64_t)v0 * p.cb;
-    const uint8_t* sbase = p.es + (int64_t)v0 * p.sb;
-    const int last = p.V - 1 - v0;            // rows past the vocabulary repeat its last one
+  if (4 * spart >= p.sb) spart = 0;
+  const int cb = (int)p.cb, sb = (int)p.sb;   // a row's bytes: at most 512 and 32
+  const uint32_t coff = (uint32_t)(prow * cb + 16 * lchunk), soff = (uint32_t)(srow * sb + 4 * spart);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds + wave * 1024, lds1 = (uint32_t)(uintptr_t)lds + TL::kCodes + wave * 256;
+  auto load_whole = [&](int tile, int buf) {
+    const int64_t v0 = (int64_t)tile * TL::kRows;
+    const uint8_t* cbase = p.ec + (v0 + wave * RPI) * cb;
 #pragma unroll
     for (int q = 0; q < TL::kLoads; ++q) {
-      const int j = wave + 8 * q;
-      if (TL::kPieces % 8 != 0 && j >= TL::kPieces) break;
-      const int row = min(j * RPI + prow, last);
-      lds_dma16_base(cbase, (uint32_t)(row * (int)p.cb + 16 * lchunk), dst + 1024 * j);
+      if (TL::kPieces % 8 != 0 && wave + 8 * q >= TL::kPieces) break;
+      lds_dma16_base(cbase + 8 * q * RPI * cb, coff, lds0 + buf * TL::kBytes + 8192 * q);
     }
-    if (wave < kScaleLoads) {
-      const int row = min(wave * SRPI + lane / SPR, last);
-      lds_dma16_base(sbase, (uint32_t)(row * (int)p.sb + 16 * spart), dst + TL::kCodes + 1024 * wave);
-    }
+    lds_dma4_base(p.es + (v0 + wave * SRPI) * sb, soff, lds1 + buf * TL::kBytes);
   };
-  if (t0 < t1) load_tile(t0, 0);
+  auto load_last = [&](int tile, int buf) {   // rows past the vocabulary repeat its last one
+    const int v0 = tile * TL::kRows, last = p.V - 1 - v0;
+#pragma unroll
+    for (int q = 0; q < TL::kLoads; ++q) {
+      if (TL::kPieces % 8 != 0 && wave + 8 * q >= TL::kPieces) break;
+      lds_dma16_base(p.ec + (int64_t)v0 * cb, (uint32_t)(min((wave + 8 * q) * RPI + prow, last) * cb + 16 * lchunk),
+                     lds0 + buf * TL::kBytes + 8192 * q);
+    }
+    lds_dma4_base(p.es + (int64_t)v0 * sb, (uint32_t)(min(wave * SRPI + srow, last) * sb + 4 * spart),
+                  lds1 + buf * TL::kBytes);
+  };
+  // tiles t0 .. tw - 1 are whole; a last one that is not is taken on its own at the end
+  const int tw = min(t1, p.V / TL::kRows);
+  if (t0 < tw) load_whole(t0, 0);
 
   // the rows of this wave: codes, scales and target
   const int rg = wave & 3, half = wave >> 2;
@@ -244,72 +280,154 @@ __global__ __launch_bounds__(512, KS <= 8 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Par
     mx4_lane_scales<NW>(sr, h, hs);
   }
 
-  float l = 0.f, m = -INFINITY;
-  // (s log2 e) - M of a logit with the fixed shift, else s log2 e
-  auto exponent = [&](float z) { return FIXED ? capped_shifted(z, p.sc.alpha, p.sc.invK) : capped_log2(z, p.sc); };
-  // the sums of a block whose first vocabulary row is vbase (register r: row 8 (r / 4) + 4 h + r % 4)
-  auto add_block = [&](const f32x16& acc, int vbase, bool whole) {
-    if constexpr (FIXED) {
-      float part = 0.f;
-      if (whole) {
+  // Sums of the terms 2^(s log2 e - reference). Fixed shift: the reference is M. Otherwise it is m, which
+  // follows the largest logit only when one is more than 2^kSlack times the terms around 1: the sum has
+  // room for that, and the usual block costs no rescaling.
+  constexpr float kSlack = 40.f;
+  float l = 0.f, m = -1e30f;
+  auto exponent = [&](float z) {
+    if (FORM == kMx4Uncapped) return __builtin_fmaf(z, kLog2e, -m);
+    const float t = capped_shifted(z, p.sc.alpha, p.sc.invK);
+    return FIXED ? t : (p.sc.M - m) + t;
+  };
+  // before the terms of a block are added: its largest logit (the cap is monotone) against the reference
+  auto follow = [&](const f32x16& z) {
+    if (FIXED) return;
+    float top = z[0];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) part += fexp2(exponent(acc[r]));
-      } else {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float e = fexp2(exponent(acc[r]));
-          part += vbase + 8 * (r >> 2) + 4 * h + (r & 3) < p.V ? e : 0.f;
-        }
-      }
-      l += part;
-    } else {
-      float s2[16], bm = -INFINITY, nan = 0.f;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s2[r] = whole || vbase + 8 * (r >> 2) + 4 * h + (r & 3) < p.V ? exponent(acc[r]) : -INFINITY;
-        bm = fmaxf(bm, s2[r]);
-        nan += s2[r] != s2[r] ? s2[r] : 0.f;
-      }
-      const float mn = fmaxf(m, bm);
-      if (mn != -INFINITY) {
-        float part = 0.f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) part += fexp2(s2[r] - mn);
-        l = l * fexp2(m - mn) + part;
-        m = mn;
-      } else {
-        l += nan;
-      }
+    for (int r = 1; r < 16; ++r) top = fmaxf(top, z[r]);
+    const float s2 = FORM == kMx4Capped ? p.sc.M + capped_shifted(top, p.sc.alpha, p.sc.invK) : top * kLog2e;
+    if (__any(s2 > m + kSlack)) {
+      const float mn = fmaxf(m, s2);
+      l *= fexp2(m - mn);
+      m = mn;
     }
   };
 
-  for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) & 1;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's part of tile t has landed
-    __syncthreads();                                   // and everyone's; the other buffer is free
-    if (t + 1 < t1) load_tile(t + 1, buf ^ 1);
-    const lds_char* tile = lds + buf * TL::kBytes;
+  // Software pipeline: the chain of a block's steps runs between the terms of the block before it, and
+  // fragments are read from LDS kAhead steps before their use, across blocks and tiles. The barrier that
+  // publishes the next tile therefore stands kAhead steps before a tile's end: there every read of this
+  // tile has been issued and waited for, so its buffer also takes the tile after the next.
+  constexpr int kAhead = 1;
+  constexpr int kPerStep = (16 + KS - 1) / KS;   // terms added per step
+  // LDS addresses of this lane's fragment of each step in buffer 0, block 0: the others are a constant away
+  // (blocks start at multiples of 64 rows, whole periods of the swizzle)
+  const lds_char* fptr[KS];
 #pragma unroll
+  for (int k = 0; k < KS; ++k)
+    fptr[k] = lds + (half * 32 + col) * TL::kRowBytes + (((2 * k + h) ^ TL::swizzle(half * 32 + col)) * 16);
+  const lds_char* sptr = lds + TL::kCodes + (half * 32 + col) * TL::kScaleBytes;
+  typedef const __attribute__((address_space(3))) i32x4* frag_ptr;
+  i32x4 next[kAhead], nscale[NS];
+
+  f32x16 prev;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) prev[r] = -INFINITY;
+  if (FIXED && t0 < tw) {   // there is no block before the first one: what its terms will add is taken off here
+    const float none = fexp2(exponent(-INFINITY));
+#pragma unroll
+    for (int r = 0; r < 16; ++r) l -= none;
+  }
+  // block B of tile t, which is in buffer BUF, into acc, adding the terms of `before`
+  auto block = [&](auto buf_, auto b_, int t, f32x16& acc, const f32x16& before) {
+    constexpr int BUF = decltype(buf_)::value, B = decltype(b_)::value;
+    constexpr bool LAST = B + 1 == TL::kBlocksPerWave;
+    constexpr int NBUF = LAST ? BUF ^ 1 : BUF, NB = LAST ? 0 : B + 1;   // the block after this one
+    constexpr int at = BUF * TL::kBytes + B * 64 * TL::kRowBytes;
+    constexpr int nat = NBUF * TL::kBytes + NB * 64 * TL::kRowBytes;
+    constexpr int snat = NBUF * TL::kBytes + NB * 64 * TL::kScaleBytes;
+    i32x4 fr[KS];
+    int sa[NW];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) fr[k] = next[k];
+    mx4_lane_scales<NW>(nscale, h, sa);
+    follow(before);
+    acc = f32x16{};
+    float part = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      if (k == KS - kAhead) {
+        if (LAST) {
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // tile t + 1 has landed, tile t is read
+          __syncthreads();
+          load_whole(min(t + 2, tw - 1), BUF);   // (past the end a tile that no one reads: no branch here)
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) nscale[i] = *(frag_ptr)(sptr + snat + 16 * i);
+      }
+      if (k + kAhead < KS) fr[k + kAhead] = *(frag_ptr)(fptr[k + kAhead] + at);
+      else next[k + kAhead - KS] = *(frag_ptr)(fptr[k + kAhead - KS] + nat);
+      acc = mx4_step(k, fr[k], sa, hf[k], hs, acc);
+#pragma unroll
+      for (int r = k * kPerStep; r < (k + 1) * kPerStep && r < 16; ++r) part += fexp2(exponent(before[r]));
+      asm volatile("" ::"v"(part));   // a use of the sum here keeps its terms between the MFMAs
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    asm volatile("" : "+v"(acc));   // the chain stays in its block
+    l += part;
+  };
+  auto tile = [&](auto buf_, int t) {
+    f32x16 a0;
+    block(buf_, std::integral_constant<int, 0>{}, t, a0, prev);
+    if (!FIXED && t == t0) l = 0.f;              // there was no block before
+    if constexpr (TL::kBlocksPerWave == 2) block(buf_, std::integral_constant<int, 1>{}, t, prev, a0);
+    else prev = a0;
+  };
+  auto add = [&](const f32x16& z, int vbase) {   // a block on its own; rows past the vocabulary drop out
+    // (register r: vocabulary row 8 (r / 4) + 4 h + r % 4 of the block)
+    f32x16 y = z;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) y[r] = vbase + 8 * (r >> 2) + 4 * h + (r & 3) < p.V ? z[r] : -INFINITY;
+    follow(y);
+    float part = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const float e = fexp2(exponent(y[r]));
+      part += vbase + 8 * (r >> 2) + 4 * h + (r & 3) < p.V ? e : 0.f;
+    }
+    l += part;
+  };
+
+  if (t0 < tw) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    load_whole(min(t0 + 1, tw - 1), 1);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) nscale[i] = *(frag_ptr)(sptr + 16 * i);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) next[k] = *(frag_ptr)(fptr[k]);
+    for (int t = t0;;) {
+      tile(std::integral_constant<int, 0>{}, t);
+      if (++t >= tw) break;
+      tile(std::integral_constant<int, 1>{}, t);
+      if (++t >= tw) break;
+    }
+    add(prev, (tw - 1) * TL::kRows + (TL::kBlocksPerWave - 1) * 64 + half * 32);
+  }
+  if (tw < t1) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();                             // nothing is in flight to buffer 0, and no one reads it
+    load_last(tw, 0);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
     for (int b = 0; b < TL::kBlocksPerWave; ++b) {
-      const int r0 = (2 * b + half) * 32;
-      const int vbase = t * TL::kRows + r0;
-      if (vbase >= p.V) continue;
-      const int lrow = r0 + col;
-      const int sw = TL::swizzle(lrow);
-      i32x4 a[KS], sr[NS];
+      const int vbase = tw * TL::kRows + b * 64 + half * 32;
+      if (vbase >= p.V) break;
+      i32x4 sr[NS];
       int sa[NW];
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
-        sr[i] = *(const __attribute__((address_space(3))) i32x4*)(tile + TL::kCodes + lrow * TL::kScaleBytes + 16 * i);
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-        a[k] = *(const __attribute__((address_space(3))) i32x4*)(tile + lrow * TL::kRowBytes + (((2 * k + h) ^ sw) * 16));
+      for (int i = 0; i < NS; ++i) sr[i] = *(frag_ptr)(sptr + b * 64 * TL::kScaleBytes + 16 * i);
       mx4_lane_scales<NW>(sr, h, sa);
       f32x16 acc = {};
-      mx4_chain<KS, NW>(a, sa, hf, hs, acc);
-      add_block(acc, vbase, vbase + 32 <= p.V);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const i32x4 a = *(frag_ptr)(fptr[k] + b * 64 * TL::kRowBytes);
+        acc = mx4_step(k, a, sa, hf[k], hs, acc);
+      }
+      add(acc, vbase);
     }
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy to LDS outlives the workgroup
 
   // the other half of the lanes, then the other wave of these rows
   lse_merge(m, l, __shfl_xor(m, 32), __shfl_xor(l, 32));
@@ -339,25 +457,28 @@ __global__ __launch_bounds__(512, KS <= 8 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Par
       sr[i] = 16 * i < p.sb ? reinterpret_cast<const i32x4*>(p.es + v * p.sb)[i] : i32x4{};
     mx4_lane_scales<NW>(sr, h, sa);
     f32x16 acc = {};
-    mx4_chain<KS, NW>(a, sa, hf, hs, acc);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) acc = mx4_step(k, a[k], sa, hf[k], hs, acc);
     const int ri = 4 * (col >> 3) + (col & 3);   // register of row col, in the lane half (col >> 2) & 1
     float z = acc[0];
 #pragma unroll
     for (int r = 1; r < 16; ++r) z = ri == r ? acc[r] : z;
     const float z2 = __shfl_xor(z, 32);
     z = ((col >> 2) & 1) == h ? z : z2;
-    // with the fixed shift, log2 of the very term that the sum added
-    if (ok) sy = FIXED ? flog2(fexp2(exponent(z))) : exponent(z);
+    // the exponent of the very term that the sum added (through exp2 and log2, so that a sum of that term
+    // alone gives 0), but where the term is too small for a float
+    const float x = exponent(z);
+    if (ok) sy = FIXED || x > -100.f ? flog2(fexp2(x)) : x;
   }
   if (h != 0 || tok >= n) return;
   if (S == 1) {
-    const float lse2 = (FIXED ? p.sc.M : m) + flog2(l);
-    p.nats[row] = kLn2 * (FIXED ? log2_ratio(l, sy) : lse2 - sy);
-    if (p.lse) p.lse[row] = kLn2 * lse2;
+    p.nats[row] = kLn2 * log2_ratio(l, sy);
+    if (p.lse) p.lse[row] = kLn2 * ((FIXED ? p.sc.M : m) + flog2(l));
   } else {
-    p.part_l[(int64_t)split * n + tok] = l;
-    if (!FIXED) p.part_m[(int64_t)split * n + tok] = m;
-    if (split == 0) p.s_target[tok] = sy;
+    const int64_t at = tok * mx4_split_stride(S) + split;
+    p.part_l[at] = l;
+    if (!FIXED) p.part_m[at] = m;
+    if (split == 0) p.s_target[tok] = FIXED ? sy : m + sy;
   }
 }
 
@@ -370,24 +491,43 @@ __global__ __launch_bounds__(256) void fwd_mx4_finalize_kernel(FwdMx4Params p, i
   const int S = mx4_splits(n, (p.V + tile - 1) / tile, p.grid);
   if (direct && S == 1) return;
   const int64_t r = p.rows ? (int64_t)p.rows[i] : i;
-  if (fixed) {
-    float l = 0.f;
-    for (int s = 0; s < S; ++s) l += p.part_l[(int64_t)s * n + i];
-    p.nats[r] = kLn2 * log2_ratio(l, p.s_target[i]);
-    if (p.lse) p.lse[r] = kLn2 * (p.sc.M + flog2(l));
-    return;
+  const int stride = mx4_split_stride(S);
+  const float* pl = p.part_l + i * stride;
+  const float* pm = p.part_m + i * stride;
+  const float sy = p.s_target[i];
+  float m = p.sc.M, l = 0.f;   // M is the fixed shift's reference
+  if (!fixed) m = -INFINITY;
+  // eight splits at a time, so that their loads' latencies overlap
+  int s = 0;
+  for (; s + 8 <= S; s += 8) {
+    const float4 l0 = *reinterpret_cast<const float4*>(pl + s), l1 = *reinterpret_cast<const float4*>(pl + s + 4);
+    if (fixed) {
+      l += ((l0.x + l0.y) + (l0.z + l0.w)) + ((l1.x + l1.y) + (l1.z + l1.w));
+    } else {
+      const float4 m0 = *reinterpret_cast<const float4*>(pm + s), m1 = *reinterpret_cast<const float4*>(pm + s + 4);
+      lse_merge(m, l, m0.x, l0.x);
+      lse_merge(m, l, m0.y, l0.y);
+      lse_merge(m, l, m0.z, l0.z);
+      lse_merge(m, l, m0.w, l0.w);
+      lse_merge(m, l, m1.x, l1.x);
+      lse_merge(m, l, m1.y, l1.y);
+      lse_merge(m, l, m1.z, l1.z);
+      lse_merge(m, l, m1.w, l1.w);
+    }
   }
-  float m = -INFINITY, l = 0.f;
-  for (int s = 0; s < S; ++s) lse_merge(m, l, p.part_m[(int64_t)s * n + i], p.part_l[(int64_t)s * n + i]);
-  const float lse2 = m + flog2(l);
-  p.nats[r] = kLn2 * (lse2 - p.s_target[i]);
-  if (p.lse) p.lse[r] = kLn2 * lse2;
+  for (; s < S; ++s) {
+    if (fixed) l += pl[s];
+    else lse_merge(m, l, pm[s], pl[s]);
+  }
+  p.nats[r] = kLn2 * (fixed ? log2_ratio(l, sy) : not_below_zero(m + flog2(l) - sy));
+  if (p.lse) p.lse[r] = kLn2 * (m + flog2(l));
 }
 
 template <int KS>
 static void launch_fwd_mx4_ks(const FwdMx4Params& p, hipStream_t st) {
-  if (p.sc.fixed) hipLaunchKernelGGL((fwd_mx4_kernel<KS, true>), dim3(p.grid), dim3(512), 0, st, p);
-  else hipLaunchKernelGGL((fwd_mx4_kernel<KS, false>), dim3(p.grid), dim3(512), 0, st, p);
+  if (p.sc.fixed) hipLaunchKernelGGL((fwd_mx4_kernel<KS, kMx4Fixed>), dim3(p.grid), dim3(512), 0, st, p);
+  else if (p.sc.c > 0.f) hipLaunchKernelGGL((fwd_mx4_kernel<KS, kMx4Capped>), dim3(p.grid), dim3(512), 0, st, p);
+  else hipLaunchKernelGGL((fwd_mx4_kernel<KS, kMx4Uncapped>), dim3(p.grid), dim3(512), 0, st, p);
 }
 
 hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const uint8_t* ecodes,
