@@ -171,6 +171,9 @@ class _Args:
         return t
 
     def same_device(self):
+        index = self.seen[0][1].get_device()   # negative off the GPU
+        if index >= 0 and all(t.get_device() == index for _, t in self.seen):
+            return
         dev = None
         for name, t in self.seen:
             if t.device.type != "cuda":
@@ -433,15 +436,25 @@ def pg_sgd_step_bf16(master: torch.Tensor, grad: torch.Tensor, lr: float, embed:
 _FLOATS = _BF16 + (torch.float32,)
 
 
+# the current stream's handle by device index: torch's own lookup where it has one (a small part of the
+# time of making a Stream object, which is a quarter of a small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _enqueue(entry: str, ref: torch.Tensor, stream, *args) -> None:
     """The library call on the device that holds the tensors, whichever is current: on `stream`, or
     on that device's current one."""
     fn = getattr(load(), entry)
-    if ref.device.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else int(stream)), entry)
+    index = ref.get_device()
+    stream = _raw_stream(index) if stream is None else int(stream)
+    if index == torch.cuda.current_device():
+        status = fn(*args, stream)
     else:
-        with torch.cuda.device(ref.device):
-            _check(fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else int(stream)), entry)
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != PG_OK:
+        _check(status, entry)
 
 
 def _norm_inputs(a: _Args, x, weight, bias, score_mask):

@@ -29,7 +29,7 @@ struct NormParams {
   const uint8_t* mask;
   int64_t T;
   int32_t D;
-  double eps;
+  double eps, inv_d;       // inv_d = 1 / D
   void* y;               // float or bf16 rows, or the codes
   uint8_t* scales;
 };
@@ -71,33 +71,59 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormParams p) {
   constexpr int RPW = 64 / LPR;
   const int lane = threadIdx.x & 63, l = lane % LPR;
   const int64_t first = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * RPW + lane / LPR;
-  float w[K][8], b[K][8];
+  const int64_t step = (int64_t)gridDim.x * 4 * RPW;
+  // held as float64 where that leaves enough registers to keep several waves per SIMD
+  typename std::conditional<K == 1, double, float>::type w[K][8], b[K][8];
 #pragma unroll
-  for (int k = 0; k < K; ++k) norm_params_chunk(p, l + k * LPR, w[k], b[k]);
-  for (int64_t t = first; t < p.T; t += (int64_t)gridDim.x * 4 * RPW) {
-    if (p.mask && !p.mask[t]) continue;
+  for (int k = 0; k < K; ++k) {
+    float wf[8], bf[8];
+    norm_params_chunk(p, l + k * LPR, wf, bf);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w[k][j] = wf[j];
+      b[k][j] = bf[j];
+    }
+  }
+  // the row after this one is on its way while this one is worked on
+  RawChunk<TX> raw[K];
+  auto fetch = [&](int64_t t) {
+    const bool scored = t < p.T && !(p.mask && !p.mask[t]);
+    if (scored) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) raw[k].load(static_cast<const TX*>(p.x) + t * p.D, l + k * LPR, p.D);
+    }
+    return scored;
+  };
+  bool scored = fetch(first);
+  for (int64_t t = first; t < p.T; t += step) {
     float x[K][8];
-    double s = 0.0;
 #pragma unroll
-    for (int k = 0; k < K; ++k) load_chunk(static_cast<const TX*>(p.x) + t * p.D, l + k * LPR, p.D, x[k]);
+    for (int k = 0; k < K; ++k) raw[k].unpack(x[k]);
+    const bool now = scored;
+    scored = fetch(t + step);
+    if (!now) continue;
+    double s = 0.0;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += (double)x[k][j];
-    const double mean = group_sum<LPR>(s) / p.D;
+    const double mean = group_sum<LPR>(s) * p.inv_d;
+    double d[K][8];
     s = 0.0;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const double d = 8 * (l + k * LPR) + j < p.D ? (double)x[k][j] - mean : 0.0;
-        s = __builtin_fma(d, d, s);
+        d[k][j] = (double)x[k][j] - mean;
+        if (8 * (l + k * LPR) + j >= p.D) d[k][j] = 0.0;
+        s = __builtin_fma(d[k][j], d[k][j], s);
       }
-    const double r = 1.0 / sqrt(group_sum<LPR>(s) / p.D + p.eps);
+    const double r = rsqrt_f64(__builtin_fma(group_sum<LPR>(s), p.inv_d, p.eps));
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float v[8];
-      norm_chunk(x[k], w[k], b[k], mean, r, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (float)__builtin_fma(d[k][j] * r, (double)w[k][j], (double)b[k][j]);
       norm_store<TOut>(p, t, l + k * LPR, v);
     }
   }
@@ -118,7 +144,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_wide_kernel(NormParams p) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += (double)x[j];
     }
-    const double mean = workgroup_sum(s, sh) / p.D;
+    const double mean = workgroup_sum(s, sh) * p.inv_d;
     s = 0.0;
     for (int c = threadIdx.x; c < nch; c += kRowThreads) {
       load_chunk(row, c, p.D, x);
@@ -128,7 +154,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_wide_kernel(NormParams p) {
         s = __builtin_fma(d, d, s);
       }
     }
-    const double r = 1.0 / sqrt(workgroup_sum(s, sh) / p.D + p.eps);
+    const double r = rsqrt_f64(__builtin_fma(workgroup_sum(s, sh), p.inv_d, p.eps));
     for (int c = threadIdx.x; c < nch; c += kRowThreads) {
       float v[8], w[8], b[8];
       load_chunk(row, c, p.D, x);
@@ -167,6 +193,7 @@ static NormParams norm_params(const void* x, const float* weight, const float* b
   p.T = T;
   p.D = D;
   p.eps = (double)eps;
+  p.inv_d = 1.0 / D;
   p.y = y;
   p.scales = scales;
   return p;
@@ -206,7 +233,7 @@ struct NormBwdParams {
   const uint8_t* mask;
   int64_t T;
   int32_t D;
-  double eps;
+  double eps, inv_d;
   void* dx;       // nullptr: not wanted
   float* part;    // partial sums of dw and db per workgroup [blocks][2][D]; nullptr: not wanted
   double* stats;  // wide rows: mean and r of each row, for the column sums
@@ -215,11 +242,17 @@ struct NormBwdParams {
 // Rows up to kRowWaveMax. Each lane keeps the sums of dw and db over its rows for its own columns; at
 // the end the waves of a workgroup add theirs in wave order through LDS, so that the result does not
 // depend on timing.
+template <int K>
+struct NormBwdShape {
+  // threads of a workgroup, at most: as many waves as share one partial sum, within the registers they need
+  static constexpr int kThreads = K == 1 ? 1024 : K == 2 ? 512 : 256;
+};
+
 template <typename TX, typename TDY, typename TDX, int LPR, int K>
-__global__ __launch_bounds__(256) void norm_bwd_rows_kernel(NormBwdParams p) {
+__global__ __launch_bounds__(NormBwdShape<K>::kThreads) void norm_bwd_rows_kernel(NormBwdParams p) {
   constexpr int RPW = 64 / LPR;
   __shared__ float sums[2][LPR * K * 8];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % LPR;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, l = lane % LPR;
   float w[K][8], dw[K][8], db[K][8];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -230,11 +263,35 @@ __global__ __launch_bounds__(256) void norm_bwd_rows_kernel(NormBwdParams p) {
       dw[k][j] = db[k][j] = 0.f;
     }
   }
-  const float invD = 1.0f / (float)p.D;
-  const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * RPW + lane / LPR;
-  for (int64_t t = first; t < p.T; t += (int64_t)gridDim.x * 4 * RPW) {
+  const float invD = (float)p.inv_d;
+  const int64_t first = ((int64_t)blockIdx.x * waves + wave) * RPW + lane / LPR;
+  const int64_t step = (int64_t)gridDim.x * waves * RPW;
+  // the row after this one is on its way while this one is worked on
+  RawChunk<TX> rx[K];
+  RawChunk<TDY> rdy[K];
+  auto fetch = [&](int64_t t) {
+    const bool scored = t < p.T && !(p.mask && !p.mask[t]);
+    if (scored) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        rx[k].load(static_cast<const TX*>(p.x) + t * p.D, l + k * LPR, p.D);
+        rdy[k].load(static_cast<const TDY*>(p.dy) + t * p.D, l + k * LPR, p.D);
+      }
+    }
+    return scored;
+  };
+  bool scored = fetch(first);
+  for (int64_t t = first; t < p.T; t += step) {
     TDX* dxrow = static_cast<TDX*>(p.dx) + t * p.D;
-    if (p.mask && !p.mask[t]) {
+    float x[K][8], dy[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      rx[k].unpack(x[k]);
+      rdy[k].unpack(dy[k]);
+    }
+    const bool now = scored;
+    scored = fetch(t + step);
+    if (!now) {
       if (p.dx) {
         const float zero[8] = {};
 #pragma unroll
@@ -242,28 +299,23 @@ __global__ __launch_bounds__(256) void norm_bwd_rows_kernel(NormBwdParams p) {
       }
       continue;
     }
-    float x[K][8], dy[K][8];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      load_chunk(static_cast<const TX*>(p.x) + t * p.D, l + k * LPR, p.D, x[k]);
-      load_chunk(static_cast<const TDY*>(p.dy) + t * p.D, l + k * LPR, p.D, dy[k]);
-    }
     double s = 0.0;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += (double)x[k][j];
-    const double mean = group_sum<LPR>(s) / p.D;
+    const double mean = group_sum<LPR>(s) * p.inv_d;
     s = 0.0;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const double d = 8 * (l + k * LPR) + j < p.D ? (double)x[k][j] - mean : 0.0;
+        double d = (double)x[k][j] - mean;
+        if (8 * (l + k * LPR) + j >= p.D) d = 0.0;
         x[k][j] = (float)d;
         s = __builtin_fma(d, d, s);
       }
-    const float r = (float)(1.0 / sqrt(group_sum<LPR>(s) / p.D + p.eps));
+    const float r = (float)rsqrt_f64(__builtin_fma(group_sum<LPR>(s), p.inv_d, p.eps));
     float c1 = 0.f, c2 = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -299,14 +351,14 @@ __global__ __launch_bounds__(256) void norm_bwd_rows_kernel(NormBwdParams p) {
         db[k][j] += __shfl_xor(db[k][j], off);
       }
     }
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < waves; ++q) {
     if (wave == q && lane < LPR) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float* a = &sums[0][(l + k * LPR) * 8 + j];
-          float* b = &sums[1][(l + k * LPR) * 8 + j];
+          float* a = &sums[0][(j * K + k) * LPR + l];   // lanes side by side: no two in one bank
+          float* b = &sums[1][(j * K + k) * LPR + l];
           *a = q ? *a + dw[k][j] : dw[k][j];
           *b = q ? *b + db[k][j] : db[k][j];
         }
@@ -314,9 +366,10 @@ __global__ __launch_bounds__(256) void norm_bwd_rows_kernel(NormBwdParams p) {
     __syncthreads();
   }
   float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
-  for (int d = threadIdx.x; d < p.D; d += 256) {
-    part[d] = sums[0][d];
-    part[p.D + d] = sums[1][d];
+  for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
+    const int c = d >> 3, at = ((d & 7) * K + c / LPR) * LPR + c % LPR;
+    part[d] = sums[0][at];
+    part[p.D + d] = sums[1][at];
   }
 }
 
@@ -344,7 +397,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_bwd_wide_kernel(NormBwdParam
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += (double)x[j];
     }
-    const double mean = workgroup_sum(s, sh) / p.D;
+    const double mean = workgroup_sum(s, sh) * p.inv_d;
     double c1 = 0.0, c2 = 0.0;
     s = 0.0;
     for (int c = threadIdx.x; c < nch; c += kRowThreads) {
@@ -360,9 +413,9 @@ __global__ __launch_bounds__(kRowThreads) void norm_bwd_wide_kernel(NormBwdParam
         c2 = __builtin_fma(g, d, c2);
       }
     }
-    const double r = 1.0 / sqrt(workgroup_sum(s, sh) / p.D + p.eps);
-    c1 = workgroup_sum(c1, sh) / p.D;
-    c2 = workgroup_sum(c2, sh) * r / p.D;
+    const double r = rsqrt_f64(__builtin_fma(workgroup_sum(s, sh), p.inv_d, p.eps));
+    c1 = workgroup_sum(c1, sh) * p.inv_d;
+    c2 = workgroup_sum(c2, sh) * r * p.inv_d;
     if (p.stats && threadIdx.x == 0) {
       p.stats[2 * t] = mean;
       p.stats[2 * t + 1] = r;
@@ -418,9 +471,19 @@ __global__ __launch_bounds__(kNormSumThreads) void norm_bwd_sum_kernel(const flo
   __shared__ double sh[kNormSumThreads / 64][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t i = (int64_t)blockIdx.x * 64 + lane, n = 2 * (int64_t)D;
+  constexpr int kWaves = kNormSumThreads / 64, kBatch = 8;   // loads of a batch are in flight together
   double s = 0.0;
-  if (i < n)
-    for (int b = wave; b < blocks; b += kNormSumThreads / 64) s += (double)part[b * n + i];
+  if (i < n) {
+    int b = wave;
+    for (; b + (kBatch - 1) * kWaves < blocks; b += kBatch * kWaves) {
+      float v[kBatch];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) v[q] = part[(int64_t)(b + q * kWaves) * n + i];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) s += (double)v[q];
+    }
+    for (; b < blocks; b += kWaves) s += (double)part[(int64_t)b * n + i];
+  }
   sh[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && i < n) {
@@ -433,7 +496,7 @@ __global__ __launch_bounds__(kNormSumThreads) void norm_bwd_sum_kernel(const flo
   }
 }
 
-constexpr int kNormBwdBlocks = 512;     // workgroups of the backward, and partial sums
+constexpr int kNormBwdBlocks = 256;     // workgroups of the backward, and partial sums: one per CU
 constexpr int kNormColumnRows = 64;     // rows of T that split the column sums of wide rows, at most
 
 NormBwdWorkspace norm_bwd_workspace(int64_t T, int32_t D) {
@@ -459,9 +522,13 @@ static void launch_norm_bwd_t(const NormBwdParams& p, int& blocks, hipStream_t s
   }
 #define PG_NORM_BWD(LPR, K)                                                                                      \
   {                                                                                                              \
-    const int64_t need = (p.T + 4 * (64 / LPR) - 1) / (4 * (64 / LPR));                                           \
+    /* waves of a workgroup: four where that keeps every workgroup at work, up to the most where rows are many */ \
+    const int64_t rows = (p.T + 64 / LPR - 1) / (64 / LPR);                                                       \
+    int waves = 4;                                                                                                \
+    while (waves < NormBwdShape<K>::kThreads / 64 && rows > (int64_t)waves * kNormBwdBlocks) waves *= 2;          \
+    const int64_t need = (rows + waves - 1) / waves;                                                              \
     blocks = (int)(need < kNormBwdBlocks ? need : kNormBwdBlocks);                                                \
-    hipLaunchKernelGGL((norm_bwd_rows_kernel<TX, TDY, TDX, LPR, K>), dim3(blocks), dim3(256), 0, st, p);         \
+    hipLaunchKernelGGL((norm_bwd_rows_kernel<TX, TDY, TDX, LPR, K>), dim3(blocks), dim3(64 * waves), 0, st, p);   \
   }
   if (D <= 128) PG_NORM_BWD(16, 1)
   else if (D <= 256) PG_NORM_BWD(32, 1)
@@ -483,6 +550,7 @@ hipError_t launch_norm_bwd(const void* x, int32_t dtype_x, const float* weight, 
   p.T = T;
   p.D = D;
   p.eps = (double)eps;
+  p.inv_d = 1.0 / D;
   p.dx = dx;
   if (dweight || dbias) {
     p.part = reinterpret_cast<float*>(ws + L.part);

@@ -78,12 +78,77 @@ __device__ __forceinline__ void store_chunk(uint16_t* row, int c, int D, const f
   }
 }
 
-// Sum over a group of LPR lanes, the same value in each (a butterfly: a fixed order).
+// A chunk as it lies in memory, so that a load can be held in flight and unpacked when it is used.
+template <typename T>
+struct RawChunk;
+template <>
+struct RawChunk<uint16_t> {
+  u32x4 a;
+  __device__ __forceinline__ void load(const uint16_t* row, int c, int D) {
+    if (8 * c + 8 <= D) {
+      a = *reinterpret_cast<const u32x4_a2*>(row + 8 * (int64_t)c);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = 8 * c + 2 * j < D ? row[8 * (int64_t)c + 2 * j] : 0u;
+        const uint32_t hi = 8 * c + 2 * j + 1 < D ? row[8 * (int64_t)c + 2 * j + 1] : 0u;
+        a[j] = lo | hi << 16;
+      }
+    }
+  }
+  __device__ __forceinline__ void unpack(float* v) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(a[j] << 16);
+      v[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct RawChunk<float> {
+  float f[8];
+  __device__ __forceinline__ void load(const float* row, int c, int D) { load_chunk(row, c, D, f); }
+  __device__ __forceinline__ void unpack(float* v) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f[j];
+  }
+};
+
+// v of the lane that a DPP pattern names, in both halves of a double.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  const int i = __builtin_bit_cast(int, v);
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, 0xf, 0xf, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const int lo = __double2loint(v), hi = __double2hiint(v);
+  return __hiloint2double(__builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xf, 0xf, false),
+                          __builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xf, 0xf, false));
+}
+
+// Sum over a group of LPR lanes, the same value in each, in a fixed order: within 16 lanes by lane
+// patterns of the VALU (the neighbour, the other pair of a quad, the mirrored quad and eight), which need
+// no LDS round trip; a lane exchange beyond.
 template <int LPR, typename T>
 __device__ __forceinline__ T group_sum(T v) {
+  static_assert(LPR >= 16, "runs of 16 lanes");
+  v += dpp<0xB1>(v);    // quad_perm 1, 0, 3, 2
+  v += dpp<0x4E>(v);    // quad_perm 2, 3, 0, 1
+  v += dpp<0x141>(v);   // row_half_mirror
+  v += dpp<0x140>(v);   // row_mirror
 #pragma unroll
-  for (int off = LPR / 2; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+  for (int off = 16; off < LPR; off <<= 1) v += __shfl_xor(v, off);
   return v;
+}
+
+// 1 / sqrt(v) in float64: the hardware's approximation (at least 20 bits) and two Newton steps, each of
+// which doubles the bits. 0 gives NaN (an infinity times zero in the steps).
+__device__ __forceinline__ double rsqrt_f64(double v) {
+  double r = __builtin_amdgcn_rsq(v);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = r * __builtin_fma(-0.5 * v * r, r, 1.5);
+  return r;
 }
 
 // Sum over a workgroup of kRowThreads threads, the same value in each: the waves' sums in wave order.
