@@ -7,6 +7,7 @@
 // bytes) and its scale bytes to 16, so that every row starts on 16 bytes.
 #pragma once
 #include "pg_common.h"
+#include "pg_rows.h"
 
 namespace pg {
 
@@ -59,15 +60,15 @@ __device__ __forceinline__ void mx4_store_chunk(const float* v, int c, int D, ui
     const uint32_t b = __float_as_uint(v[j]) & 0x7fffffffu;
     a = b > a ? b : a;
   }
-#pragma unroll
-  for (int off = 1; off < 4; off <<= 1) {
-    const uint32_t b = (uint32_t)__shfl_xor((int)a, off);
-    a = b > a ? b : a;
-  }
-  const uint32_t s = mx4_scale_byte(a);
+  uint32_t o = dpp<0xB1>(a);   // quad_perm 1, 0, 3, 2
+  a = o > a ? o : a;
+  o = dpp<0x4E>(a);            // quad_perm 2, 3, 0, 1
+  a = o > a ? o : a;
+  const uint32_t s = 8 * c < D ? mx4_scale_byte(a) : 0u;
   const uint32_t code = s == 255u ? 0u : mx4_encode8(v, mx4_scale_value(s));
-  uint32_t w = s | (uint32_t)__shfl_down((int)s, 4) << 8;   // the scales of blocks b, b + 1 in lane 4 b
-  w |= (uint32_t)__shfl_down((int)w, 8) << 16;               // of blocks b .. b + 3
+  // the scales of blocks b, b + 1 in lane 4 b, then of b .. b + 3 (the lanes 4 and 8 further in the run)
+  uint32_t w = s | dpp<0x104>(s) << 8;
+  w |= dpp<0x108>(w) << 16;
   const int nch = (D + 7) >> 3;
   if (c < 8 * ((D + 63) >> 6)) *reinterpret_cast<uint32_t*>(codes + 4 * (int64_t)c) = code;
   if ((c & 15) == 0 && c < nch) {

@@ -55,9 +55,10 @@ __device__ __forceinline__ void norm_chunk(const float* x, const float* w, const
 template <typename TOut>
 __device__ __forceinline__ void norm_store(const NormParams& p, int64_t t, int c, float* v) {
   if constexpr (std::is_same<TOut, Mx4Out>::value) {
+    if (8 * c + 8 > p.D) {   // the row's padding is zero whatever its bias
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (8 * c + j >= p.D) v[j] = 0.f;   // the row's padding is zero whatever its bias
+      for (int j = 0; j < 8; ++j) v[j] = 8 * c + j < p.D ? v[j] : 0.f;
+    }
     mx4_store_chunk(v, c, p.D, static_cast<uint8_t*>(p.y) + t * mx4_code_bytes(p.D),
                     p.scales + t * mx4_scale_bytes(p.D));
   } else {
@@ -72,6 +73,7 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormParams p) {
   const int lane = threadIdx.x & 63, l = lane % LPR;
   const int64_t first = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * RPW + lane / LPR;
   const int64_t step = (int64_t)gridDim.x * 4 * RPW;
+  const bool full = p.D == LPR * K * 8;   // no lane has values past the row's end
   // held as float64 where that leaves enough registers to keep several waves per SIMD
   typename std::conditional<K == 1, double, float>::type w[K][8], b[K][8];
 #pragma unroll
@@ -115,9 +117,17 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormParams p) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         d[k][j] = (double)x[k][j] - mean;
-        if (8 * (l + k * LPR) + j >= p.D) d[k][j] = 0.0;
-        s = __builtin_fma(d[k][j], d[k][j], s);
       }
+    if (!full) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[k][j] = 8 * (l + k * LPR) + j < p.D ? d[k][j] : 0.0;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = __builtin_fma(d[k][j], d[k][j], s);
     const double r = rsqrt_f64(__builtin_fma(group_sum<LPR>(s), p.inv_d, p.eps));
 #pragma unroll
     for (int k = 0; k < K; ++k) {

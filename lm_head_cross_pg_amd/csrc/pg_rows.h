@@ -114,31 +114,50 @@ struct RawChunk<float> {
   }
 };
 
-// v of the lane that a DPP pattern names, in both halves of a double.
+// v of the lane that a DPP pattern within 16 lanes names (every lane has a partner in the patterns used
+// here), and the sum of v and that.
 template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  const int i = __builtin_bit_cast(int, v);
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, 0xf, 0xf, false));
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
 }
 template <int CTRL>
-__device__ __forceinline__ double dpp(double v) {
-  const int lo = __double2loint(v), hi = __double2hiint(v);
-  return __hiloint2double(__builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xf, 0xf, false),
-                          __builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xf, 0xf, false));
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double add_dpp(double v) {
+  return v + __hiloint2double((int)dpp<CTRL>((uint32_t)__double2hiint(v)), (int)dpp<CTRL>((uint32_t)__double2loint(v)));
+}
+// The same across the neighbouring 16 and 32 lanes: a swap of the halves of two copies leaves the lower
+// half's values in one and the upper half's in the other.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+template <int N>
+__device__ __forceinline__ u32x2 swap_lanes(uint32_t v) {
+  if constexpr (N == 16) return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
+  else return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+}
+template <int N>
+__device__ __forceinline__ float add_swapped(float v) {
+  const u32x2 s = swap_lanes<N>(__float_as_uint(v));
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+template <int N>
+__device__ __forceinline__ double add_swapped(double v) {
+  const u32x2 lo = swap_lanes<N>((uint32_t)__double2loint(v)), hi = swap_lanes<N>((uint32_t)__double2hiint(v));
+  return __hiloint2double((int)hi[0], (int)lo[0]) + __hiloint2double((int)hi[1], (int)lo[1]);
 }
 
-// Sum over a group of LPR lanes, the same value in each, in a fixed order: within 16 lanes by lane
-// patterns of the VALU (the neighbour, the other pair of a quad, the mirrored quad and eight), which need
-// no LDS round trip; a lane exchange beyond.
+// Sum over a group of LPR lanes, the same value in each, in a fixed order, without an LDS round trip:
+// the neighbour, the other pair of the quad, the mirrored quad and eight, then 16 and 32 lanes.
 template <int LPR, typename T>
 __device__ __forceinline__ T group_sum(T v) {
   static_assert(LPR >= 16, "runs of 16 lanes");
-  v += dpp<0xB1>(v);    // quad_perm 1, 0, 3, 2
-  v += dpp<0x4E>(v);    // quad_perm 2, 3, 0, 1
-  v += dpp<0x141>(v);   // row_half_mirror
-  v += dpp<0x140>(v);   // row_mirror
-#pragma unroll
-  for (int off = 16; off < LPR; off <<= 1) v += __shfl_xor(v, off);
+  v = add_dpp<0xB1>(v);    // quad_perm 1, 0, 3, 2
+  v = add_dpp<0x4E>(v);    // quad_perm 2, 3, 0, 1
+  v = add_dpp<0x141>(v);   // row_half_mirror
+  v = add_dpp<0x140>(v);   // row_mirror
+  if constexpr (LPR >= 32) v = add_swapped<16>(v);
+  if constexpr (LPR >= 64) v = add_swapped<32>(v);
   return v;
 }
 
