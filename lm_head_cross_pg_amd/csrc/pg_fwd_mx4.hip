@@ -24,6 +24,8 @@ struct FwdMx4Params {
   int V;
   int nblocks;            // 32-row blocks of the vocabulary
   int grid;               // workgroups that share rows and splits
+  int rows_per_wg;
+  int splits;             // of the vocabulary; 0: from the row count and the grid
   Softcap sc;
   float* nats;
   float* lse;
@@ -32,15 +34,14 @@ struct FwdMx4Params {
   float* s_target;
 };
 
-// Rows of one workgroup: four waves of 32.
-constexpr int kMx4RowsPerWG = 128;
-
-// Vocabulary splits: as many as the grid has workgroups for each row tile, at most one per block.
-__host__ __device__ __forceinline__ int mx4_splits(int64_t n, int nblocks, int grid) {
-  const int64_t rt = (n + kMx4RowsPerWG - 1) / kMx4RowsPerWG;
+// Vocabulary splits where only the device knows the row count: as many as the grid has workgroups for each
+// row tile, at most one per tile of the vocabulary.
+__host__ __device__ __forceinline__ int mx4_splits(const FwdMx4Params& p, int64_t n, int ntiles) {
+  if (p.splits > 0) return p.splits;
+  const int64_t rt = (n + p.rows_per_wg - 1) / p.rows_per_wg;
   if (rt <= 0) return 1;
-  const int64_t s = grid / rt;
-  return s < 1 ? 1 : (s > nblocks ? nblocks : (int)s);
+  const int64_t s = p.grid / rt;
+  return s < 1 ? 1 : (s > ntiles ? ntiles : (int)s);
 }
 
 // The target's term is one of the sum's, so a negative difference is a rounding (NaN passes).
@@ -61,10 +62,10 @@ __global__ __launch_bounds__(256) void fwd_mx4_stream_kernel(FwdMx4Params p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, col = lane & 31;
   const int64_t n = p.n_dev ? (int64_t)(*p.n_dev) : p.n_host;
-  const int S = mx4_splits(n, p.nblocks, p.grid);
+  const int S = mx4_splits(p, n, p.nblocks);
   const int64_t rt = blockIdx.x / S;
   const int split = blockIdx.x % S;
-  const int64_t tok0 = rt * kMx4RowsPerWG + wave * 32;
+  const int64_t tok0 = rt * 128 + wave * 32;
   if (tok0 >= n) return;
   const int per = (p.nblocks + S - 1) / S;
   const int b0 = split * per, b1 = min(b0 + per, p.nblocks);
@@ -203,24 +204,24 @@ __device__ __forceinline__ f32x16 mx4_step(int k, const i32x4& a, const int* sa,
 // reference that follows the largest logit).
 enum Mx4Form { kMx4Fixed, kMx4Uncapped, kMx4Capped };
 
-template <int KS, Mx4Form FORM>
-__global__ __launch_bounds__(512, KS <= 8 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Params p) {
+template <int KS, int RB, Mx4Form FORM>
+__global__ __launch_bounds__(512, KS <= 8 && RB == 1 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Params p) {
   using TL = Mx4Tile<KS>;
   constexpr bool FIXED = FORM == kMx4Fixed;
   constexpr int NW = (KS + 3) / 4;          // words of a lane's scales
   constexpr int NS = TL::kScaleBytes / 16;
   __shared__ __attribute__((aligned(1024))) char smem[2 * TL::kBytes];
-  __shared__ float merge[2][4][32];
+  __shared__ float merge[2][RB][4][32];
   const lds_char* lds = (const lds_char*)smem;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, col = lane & 31;
   const int64_t n = p.n_dev ? (int64_t)(*p.n_dev) : p.n_host;
   const int ntiles = (p.V + TL::kRows - 1) / TL::kRows;
-  const int S = mx4_splits(n, ntiles, p.grid);
+  const int S = mx4_splits(p, n, ntiles);
   const int64_t rt = blockIdx.x / S;
   const int split = blockIdx.x % S;
-  if (rt * kMx4RowsPerWG >= n) return;
+  if (rt * (128 * RB) >= n) return;
   const int per = (ntiles + S - 1) / S;
   const int t0 = split * per, t1 = min(t0 + per, ntiles);
 
@@ -262,45 +263,54 @@ __global__ __launch_bounds__(512, KS <= 8 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Par
   const int tw = min(t1, p.V / TL::kRows);
   if (t0 < tw) load_whole(t0, 0);
 
-  // the rows of this wave: codes, scales and target
+  // the rows of this wave: codes and scales
   const int rg = wave & 3, half = wave >> 2;
-  const int64_t tok = rt * kMx4RowsPerWG + rg * 32 + col;
-  const int64_t ic = tok < n ? tok : n - 1;
-  const int64_t row = p.rows ? (int64_t)p.rows[ic] : ic;
-  i32x4 hf[KS];
-  int hs[NW];
-  {
+  auto token = [&](int rb) { return rt * (128 * RB) + (rg * RB + rb) * 32 + col; };
+  auto row_of = [&](int rb) {
+    const int64_t tok = token(rb), i = tok < n ? tok : n - 1;
+    return p.rows ? (int64_t)p.rows[i] : i;
+  };
+  i32x4 hf[RB][KS];
+  int hs[RB][NW];
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    const int64_t row = row_of(rb);
     const i32x4* src = reinterpret_cast<const i32x4*>(p.hc + row * p.cb + 16 * h);
 #pragma unroll
-    for (int k = 0; k < KS; ++k) hf[k] = k < p.steps ? src[2 * k] : i32x4{};
+    for (int k = 0; k < KS; ++k) hf[rb][k] = k < p.steps ? src[2 * k] : i32x4{};
     i32x4 sr[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i)
       sr[i] = 16 * i < p.sb ? reinterpret_cast<const i32x4*>(p.hs + row * p.sb)[i] : i32x4{};
-    mx4_lane_scales<NW>(sr, h, hs);
+    mx4_lane_scales<NW>(sr, h, hs[rb]);
   }
 
   // Sums of the terms 2^(s log2 e - reference). Fixed shift: the reference is M. Otherwise it is m, which
   // follows the largest logit only when one is more than 2^kSlack times the terms around 1: the sum has
   // room for that, and the usual block costs no rescaling.
   constexpr float kSlack = 40.f;
-  float l = 0.f, m = -1e30f;
-  auto exponent = [&](float z) {
-    if (FORM == kMx4Uncapped) return __builtin_fmaf(z, kLog2e, -m);
+  float l[RB], m[RB];
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    l[rb] = 0.f;
+    m[rb] = -1e30f;
+  }
+  auto exponent = [&](int rb, float z) {
+    if (FORM == kMx4Uncapped) return __builtin_fmaf(z, kLog2e, -m[rb]);
     const float t = capped_shifted(z, p.sc.alpha, p.sc.invK);
-    return FIXED ? t : (p.sc.M - m) + t;
+    return FIXED ? t : (p.sc.M - m[rb]) + t;
   };
   // before the terms of a block are added: its largest logit (the cap is monotone) against the reference
-  auto follow = [&](const f32x16& z) {
+  auto follow = [&](int rb, const f32x16& z) {
     if (FIXED) return;
     float top = z[0];
 #pragma unroll
     for (int r = 1; r < 16; ++r) top = fmaxf(top, z[r]);
     const float s2 = FORM == kMx4Capped ? p.sc.M + capped_shifted(top, p.sc.alpha, p.sc.invK) : top * kLog2e;
-    if (__any(s2 > m + kSlack)) {
-      const float mn = fmaxf(m, s2);
-      l *= fexp2(m - mn);
-      m = mn;
+    if (__any(s2 > m[rb] + kSlack)) {
+      const float mn = fmaxf(m[rb], s2);
+      l[rb] *= fexp2(m[rb] - mn);
+      m[rb] = mn;
     }
   };
 
@@ -309,7 +319,7 @@ __global__ __launch_bounds__(512, KS <= 8 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Par
   // publishes the next tile therefore stands kAhead steps before a tile's end: there every read of this
   // tile has been issued and waited for, so its buffer also takes the tile after the next.
   constexpr int kAhead = 1;
-  constexpr int kPerStep = (16 + KS - 1) / KS;   // terms added per step
+  constexpr int kPerStep = (16 * RB + KS - 1) / KS;   // terms added per step
   // LDS addresses of this lane's fragment of each step in buffer 0, block 0: the others are a constant away
   // (blocks start at multiples of 64 rows, whole periods of the swizzle)
   const lds_char* fptr[KS];
@@ -320,16 +330,21 @@ __global__ __launch_bounds__(512, KS <= 8 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Par
   typedef const __attribute__((address_space(3))) i32x4* frag_ptr;
   i32x4 next[kAhead], nscale[NS];
 
-  f32x16 prev;
+  typedef f32x16 Block[RB];
+  Block prev;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) prev[r] = -INFINITY;
+  for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) prev[rb][r] = -INFINITY;
   if (FIXED && t0 < tw) {   // there is no block before the first one: what its terms will add is taken off here
-    const float none = fexp2(exponent(-INFINITY));
+    const float none = fexp2(exponent(0, -INFINITY));
 #pragma unroll
-    for (int r = 0; r < 16; ++r) l -= none;
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) l[rb] -= none;
   }
   // block B of tile t, which is in buffer BUF, into acc, adding the terms of `before`
-  auto block = [&](auto buf_, auto b_, int t, f32x16& acc, const f32x16& before) {
+  auto block = [&](auto buf_, auto b_, int t, Block& acc, const Block& before) {
     constexpr int BUF = decltype(buf_)::value, B = decltype(b_)::value;
     constexpr bool LAST = B + 1 == TL::kBlocksPerWave;
     constexpr int NBUF = LAST ? BUF ^ 1 : BUF, NB = LAST ? 0 : B + 1;   // the block after this one
@@ -341,9 +356,13 @@ __global__ __launch_bounds__(512, KS <= 8 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Par
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) fr[k] = next[k];
     mx4_lane_scales<NW>(nscale, h, sa);
-    follow(before);
-    acc = f32x16{};
-    float part = 0.f;
+    float part[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      follow(rb, before[rb]);
+      acc[rb] = f32x16{};
+      part[rb] = 0.f;
+    }
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       if (k == KS - kAhead) {
@@ -357,35 +376,48 @@ __global__ __launch_bounds__(512, KS <= 8 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Par
       }
       if (k + kAhead < KS) fr[k + kAhead] = *(frag_ptr)(fptr[k + kAhead] + at);
       else next[k + kAhead - KS] = *(frag_ptr)(fptr[k + kAhead - KS] + nat);
-      acc = mx4_step(k, fr[k], sa, hf[k], hs, acc);
 #pragma unroll
-      for (int r = k * kPerStep; r < (k + 1) * kPerStep && r < 16; ++r) part += fexp2(exponent(before[r]));
-      asm volatile("" ::"v"(part));   // a use of the sum here keeps its terms between the MFMAs
+      for (int rb = 0; rb < RB; ++rb) acc[rb] = mx4_step(k, fr[k], sa, hf[rb][k], hs[rb], acc[rb]);
+#pragma unroll
+      for (int e = k * kPerStep; e < (k + 1) * kPerStep && e < 16 * RB; ++e)
+        part[e / 16] += fexp2(exponent(e / 16, before[e / 16][e % 16]));
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) asm volatile("" ::"v"(part[rb]));   // a use here keeps the terms between the MFMAs
       __builtin_amdgcn_sched_barrier(0);
     }
-    asm volatile("" : "+v"(acc));   // the chain stays in its block
-    l += part;
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      asm volatile("" : "+v"(acc[rb]));   // the chain stays in its block
+      l[rb] += part[rb];
+    }
   };
   auto tile = [&](auto buf_, int t) {
-    f32x16 a0;
+    Block a0;
     block(buf_, std::integral_constant<int, 0>{}, t, a0, prev);
-    if (!FIXED && t == t0) l = 0.f;              // there was no block before
-    if constexpr (TL::kBlocksPerWave == 2) block(buf_, std::integral_constant<int, 1>{}, t, prev, a0);
-    else prev = a0;
+    if (!FIXED && t == t0) {                     // there was no block before
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) l[rb] = 0.f;
+    }
+    if constexpr (TL::kBlocksPerWave == 2) {
+      block(buf_, std::integral_constant<int, 1>{}, t, prev, a0);
+    } else {
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) prev[rb] = a0[rb];
+    }
   };
-  auto add = [&](const f32x16& z, int vbase) {   // a block on its own; rows past the vocabulary drop out
+  auto add = [&](int rb, const f32x16& z, int vbase) {   // a block on its own; rows past the vocabulary drop out
     // (register r: vocabulary row 8 (r / 4) + 4 h + r % 4 of the block)
     f32x16 y = z;
 #pragma unroll
     for (int r = 0; r < 16; ++r) y[r] = vbase + 8 * (r >> 2) + 4 * h + (r & 3) < p.V ? z[r] : -INFINITY;
-    follow(y);
+    follow(rb, y);
     float part = 0.f;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const float e = fexp2(exponent(y[r]));
+      const float e = fexp2(exponent(rb, y[r]));
       part += vbase + 8 * (r >> 2) + 4 * h + (r & 3) < p.V ? e : 0.f;
     }
-    l += part;
+    l[rb] += part;
   };
 
   if (t0 < tw) {
@@ -402,7 +434,9 @@ __global__ __launch_bounds__(512, KS <= 8 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Par
       tile(std::integral_constant<int, 1>{}, t);
       if (++t >= tw) break;
     }
-    add(prev, (tw - 1) * TL::kRows + (TL::kBlocksPerWave - 1) * 64 + half * 32);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+      add(rb, prev[rb], (tw - 1) * TL::kRows + (TL::kBlocksPerWave - 1) * 64 + half * 32);
   }
   if (tw < t1) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -418,67 +452,76 @@ __global__ __launch_bounds__(512, KS <= 8 ? 4 : 2) void fwd_mx4_kernel(FwdMx4Par
 #pragma unroll
       for (int i = 0; i < NS; ++i) sr[i] = *(frag_ptr)(sptr + b * 64 * TL::kScaleBytes + 16 * i);
       mx4_lane_scales<NW>(sr, h, sa);
-      f32x16 acc = {};
+      Block acc = {};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const i32x4 a = *(frag_ptr)(fptr[k] + b * 64 * TL::kRowBytes);
-        acc = mx4_step(k, a, sa, hf[k], hs, acc);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) acc[rb] = mx4_step(k, a, sa, hf[rb][k], hs[rb], acc[rb]);
       }
-      add(acc, vbase);
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) add(rb, acc[rb], vbase);
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy to LDS outlives the workgroup
 
   // the other half of the lanes, then the other wave of these rows
-  lse_merge(m, l, __shfl_xor(m, 32), __shfl_xor(l, 32));
-  if (half == 1 && h == 0) {
-    merge[0][rg][col] = m;
-    merge[1][rg][col] = l;
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    lse_merge(m[rb], l[rb], __shfl_xor(m[rb], 32), __shfl_xor(l[rb], 32));
+    if (half == 1 && h == 0) {
+      merge[0][rb][rg][col] = m[rb];
+      merge[1][rb][rg][col] = l[rb];
+    }
   }
   __syncthreads();
   if (half == 1) return;
-  if constexpr (FIXED) l += merge[1][rg][col];
-  else lse_merge(m, l, merge[0][rg][col], merge[1][rg][col]);
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    if constexpr (FIXED) l[rb] += merge[1][rb][rg][col];
+    else lse_merge(m[rb], l[rb], merge[0][rb][rg][col], merge[1][rb][rg][col]);
+    const int64_t tok = token(rb), row = row_of(rb);
 
-  // The targets' logits: the wave's 32 target rows as the A operand, whose product with its 32 tokens
-  // has them on the diagonal, formed by the same instructions from the same values as the sum's.
-  float sy = __builtin_nanf("");
-  if (split == 0) {
-    const int y = p.target[row];
-    const bool ok = y >= 0 && y < p.V;
-    const int64_t v = ok ? y : 0;
-    const i32x4* src = reinterpret_cast<const i32x4*>(p.ec + v * p.cb + 16 * h);
-    i32x4 a[KS], sr[NS];
-    int sa[NW];
+    // The targets' logits: the 32 target rows as the A operand, whose product with the 32 tokens has them
+    // on the diagonal, formed by the same instructions from the same values as the sum's.
+    float sy = __builtin_nanf("");
+    if (split == 0) {
+      const int y = p.target[row];
+      const bool ok = y >= 0 && y < p.V;
+      const int64_t v = ok ? y : 0;
+      const i32x4* src = reinterpret_cast<const i32x4*>(p.ec + v * p.cb + 16 * h);
+      i32x4 a[KS], sr[NS];
+      int sa[NW];
 #pragma unroll
-    for (int k = 0; k < KS; ++k) a[k] = k < p.steps ? src[2 * k] : i32x4{};
+      for (int k = 0; k < KS; ++k) a[k] = k < p.steps ? src[2 * k] : i32x4{};
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-      sr[i] = 16 * i < p.sb ? reinterpret_cast<const i32x4*>(p.es + v * p.sb)[i] : i32x4{};
-    mx4_lane_scales<NW>(sr, h, sa);
-    f32x16 acc = {};
+      for (int i = 0; i < NS; ++i)
+        sr[i] = 16 * i < p.sb ? reinterpret_cast<const i32x4*>(p.es + v * p.sb)[i] : i32x4{};
+      mx4_lane_scales<NW>(sr, h, sa);
+      f32x16 acc = {};
 #pragma unroll
-    for (int k = 0; k < KS; ++k) acc = mx4_step(k, a[k], sa, hf[k], hs, acc);
-    const int ri = 4 * (col >> 3) + (col & 3);   // register of row col, in the lane half (col >> 2) & 1
-    float z = acc[0];
+      for (int k = 0; k < KS; ++k) acc = mx4_step(k, a[k], sa, hf[rb][k], hs[rb], acc);
+      const int ri = 4 * (col >> 3) + (col & 3);   // register of row col, in the lane half (col >> 2) & 1
+      float z = acc[0];
 #pragma unroll
-    for (int r = 1; r < 16; ++r) z = ri == r ? acc[r] : z;
-    const float z2 = __shfl_xor(z, 32);
-    z = ((col >> 2) & 1) == h ? z : z2;
-    // the exponent of the very term that the sum added (through exp2 and log2, so that a sum of that term
-    // alone gives 0), but where the term is too small for a float
-    const float x = exponent(z);
-    if (ok) sy = FIXED || x > -100.f ? flog2(fexp2(x)) : x;
-  }
-  if (h != 0 || tok >= n) return;
-  if (S == 1) {
-    p.nats[row] = kLn2 * log2_ratio(l, sy);
-    if (p.lse) p.lse[row] = kLn2 * ((FIXED ? p.sc.M : m) + flog2(l));
-  } else {
-    const int64_t at = tok * mx4_split_stride(S) + split;
-    p.part_l[at] = l;
-    if (!FIXED) p.part_m[at] = m;
-    if (split == 0) p.s_target[tok] = FIXED ? sy : m + sy;
+      for (int r = 1; r < 16; ++r) z = ri == r ? acc[r] : z;
+      const float z2 = __shfl_xor(z, 32);
+      z = ((col >> 2) & 1) == h ? z : z2;
+      // the exponent of the very term that the sum added (through exp2 and log2, so that a sum of that
+      // term alone gives 0), but where the term is too small for a float
+      const float x = exponent(rb, z);
+      if (ok) sy = FIXED || x > -100.f ? flog2(fexp2(x)) : x;
+    }
+    if (h != 0 || tok >= n) continue;
+    if (S == 1) {
+      p.nats[row] = kLn2 * log2_ratio(l[rb], sy);
+      if (p.lse) p.lse[row] = kLn2 * ((FIXED ? p.sc.M : m[rb]) + flog2(l[rb]));
+    } else {
+      const int64_t at = tok * mx4_split_stride(S) + split;
+      p.part_l[at] = l[rb];
+      if (!FIXED) p.part_m[at] = m[rb];
+      if (split == 0) p.s_target[tok] = FIXED ? sy : m[rb] + sy;
+    }
   }
 }
 
@@ -488,7 +531,7 @@ __global__ __launch_bounds__(256) void fwd_mx4_finalize_kernel(FwdMx4Params p, i
   const int64_t n = p.n_dev ? (int64_t)(*p.n_dev) : p.n_host;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
-  const int S = mx4_splits(n, (p.V + tile - 1) / tile, p.grid);
+  const int S = mx4_splits(p, n, (p.V + tile - 1) / tile);
   if (direct && S == 1) return;
   const int64_t r = p.rows ? (int64_t)p.rows[i] : i;
   const int stride = mx4_split_stride(S);
@@ -523,11 +566,19 @@ __global__ __launch_bounds__(256) void fwd_mx4_finalize_kernel(FwdMx4Params p, i
   if (p.lse) p.lse[r] = kLn2 * (m + flog2(l));
 }
 
+template <int KS, int RB>
+static void launch_fwd_mx4_rb(const FwdMx4Params& p, hipStream_t st) {
+  if (p.sc.fixed) hipLaunchKernelGGL((fwd_mx4_kernel<KS, RB, kMx4Fixed>), dim3(p.grid), dim3(512), 0, st, p);
+  else if (p.sc.c > 0.f) hipLaunchKernelGGL((fwd_mx4_kernel<KS, RB, kMx4Capped>), dim3(p.grid), dim3(512), 0, st, p);
+  else hipLaunchKernelGGL((fwd_mx4_kernel<KS, RB, kMx4Uncapped>), dim3(p.grid), dim3(512), 0, st, p);
+}
+
 template <int KS>
 static void launch_fwd_mx4_ks(const FwdMx4Params& p, hipStream_t st) {
-  if (p.sc.fixed) hipLaunchKernelGGL((fwd_mx4_kernel<KS, kMx4Fixed>), dim3(p.grid), dim3(512), 0, st, p);
-  else if (p.sc.c > 0.f) hipLaunchKernelGGL((fwd_mx4_kernel<KS, kMx4Capped>), dim3(p.grid), dim3(512), 0, st, p);
-  else hipLaunchKernelGGL((fwd_mx4_kernel<KS, kMx4Uncapped>), dim3(p.grid), dim3(512), 0, st, p);
+  if constexpr (KS <= 8) {
+    if (p.rows_per_wg == 256) return launch_fwd_mx4_rb<KS, 2>(p, st);
+  }
+  launch_fwd_mx4_rb<KS, 1>(p, st);
 }
 
 hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const uint8_t* ecodes,
@@ -562,11 +613,14 @@ hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const u
   }
   // the partial sums' room: splits x rows stays within grid x 128, and the workspace holds
   // max(ceil(T / 256), 1024) x 256 of them
-  const int64_t rt = (T + kMx4RowsPerWG - 1) / kMx4RowsPerWG;
   const int ncu = dev.cu_count > 0 ? dev.cu_count : 256;
   int tile = 32, fixed = 0, direct = 0;
+  p.rows_per_wg = 128;
   if (p.steps <= 16) {
-    const int64_t slots = 2 * ncu < 1024 ? 2 * ncu : 1024;   // workgroups that run at once
+    if (p.steps <= 8 && !mask && T >= (int64_t)256 * ncu) p.rows_per_wg = 256;
+    const int64_t rt = (T + p.rows_per_wg - 1) / p.rows_per_wg;
+    int64_t slots = p.rows_per_wg == 256 ? ncu : 2 * ncu;   // workgroups that run at once
+    if (slots > 1024) slots = 1024;
     p.grid = (int)(rt > slots ? rt : slots);
     fixed = p.sc.fixed;
     direct = 1;
@@ -587,12 +641,13 @@ hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const u
       default: launch_fwd_mx4_ks<16>(p, st); break;
     }
   } else {
+    const int64_t rt = (T + 127) / 128;
     p.grid = (int)(rt > 1024 ? rt : 1024);
     hipLaunchKernelGGL(fwd_mx4_stream_kernel, dim3(p.grid), dim3(256), 0, st, p);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (direct && !mask && mx4_splits(T, (V + tile - 1) / tile, p.grid) == 1) return hipSuccess;
+  if (direct && !mask && mx4_splits(p, T, (V + tile - 1) / tile) == 1) return hipSuccess;
   hipLaunchKernelGGL(fwd_mx4_finalize_kernel, dim3((unsigned)((T + 255) / 256)), dim3(256), 0, st, p, tile, fixed,
                      direct);
   return hipGetLastError();
