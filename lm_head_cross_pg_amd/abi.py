@@ -150,6 +150,11 @@ class _Args:
         self.seen = []
 
     def __call__(self, t, name, dtypes, numel=None, shape=None, min_numel=None, optional=False):
+        # the usual case in one expression (these checks are a large part of a small call's time)
+        if (isinstance(t, torch.Tensor) and t.dtype in dtypes and (numel is None or t.numel() == numel)
+                and (shape is None or t.shape == shape) and min_numel is None and t.is_contiguous()):
+            self.seen.append((name, t))
+            return t
         if t is None:
             if optional:
                 return None
@@ -460,9 +465,12 @@ def _enqueue(entry: str, ref: torch.Tensor, stream, *args) -> None:
 def _norm_inputs(a: _Args, x, weight, bias, score_mask):
     """x [T, D] bf16 or float32, weight and bias float32 [D] or None, score_mask uint8/bool [T] or None."""
     T, D = _matrix(a, x, "x", _FLOATS)
-    a(weight, "weight", (torch.float32,), numel=D, optional=True)
-    a(bias, "bias", (torch.float32,), numel=D, optional=True)
-    a(score_mask, "score_mask", _MASK, numel=T, optional=True)
+    if weight is not None:
+        a(weight, "weight", _F32, D)
+    if bias is not None:
+        a(bias, "bias", _F32, D)
+    if score_mask is not None:
+        a(score_mask, "score_mask", _MASK, T)
     return T, D
 
 
@@ -470,7 +478,7 @@ def pg_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Opti
                      score_mask: Optional[torch.Tensor], eps: float, y: torch.Tensor, stream=None) -> None:
     a = _Args("pg_layernorm_fwd")
     T, D = _norm_inputs(a, x, weight, bias, score_mask)
-    a(y, "y", _FLOATS, shape=(T, D))
+    a(y, "y", _FLOATS, None, (T, D))
     a.same_device()
     _enqueue(a.where, x, stream, _ptr(x), _dtype_code(x), _ptr(weight), _ptr(bias), _ptr(score_mask), T, D,
              float(eps), _ptr(y), _dtype_code(y))
@@ -492,13 +500,18 @@ def pg_mx4_scale_bytes(D: int) -> int:
     return n
 
 
-def _mx4_rows(a: _Args, codes, scales, D: int, T: Optional[int] = None, name: str = ""):
+_U8 = (torch.uint8,)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+
+
+def _mx4_rows(a: _Args, codes, scales, D: int, T: Optional[int] = None, codes_name: str = "codes",
+              scales_name: str = "scales"):
     """codes [T, 32 ceil(D / 64)] and scales [T, 16 ceil(D / 512)], uint8; returns T."""
-    a(codes, name + "codes", (torch.uint8,))
     if T is None:
-        T = codes.shape[0] if codes.dim() == 2 else -1
-    a(codes, name + "codes", (torch.uint8,), shape=(T, 32 * -(-D // 64)))
-    a(scales, name + "scales", (torch.uint8,), shape=(T, 16 * -(-D // 512)))
+        T = codes.shape[0] if isinstance(codes, torch.Tensor) and codes.dim() == 2 else -1
+    a(codes, codes_name, _U8, None, (T, 32 * -(-D // 64)))
+    a(scales, scales_name, _U8, None, (T, 16 * -(-D // 512)))
     return T
 
 
@@ -518,7 +531,7 @@ def pg_layernorm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], score_mask
                      dbias: Optional[torch.Tensor], workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     a = _Args("pg_layernorm_bwd")
     T, D = _norm_inputs(a, x, weight, None, score_mask)
-    a(dy, "dy", _FLOATS, shape=(T, D))
+    a(dy, "dy", _FLOATS, None, (T, D))
     a(dx, "dx", _FLOATS, shape=(T, D), optional=True)
     a(dweight, "dweight", (torch.float32,), numel=D, optional=True)
     a(dbias, "dbias", (torch.float32,), numel=D, optional=True)
@@ -552,12 +565,14 @@ def pg_lmhead_ce_fwd_mx4(hidden_codes: torch.Tensor, hidden_scales: torch.Tensor
                          workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     a = _Args("pg_lmhead_ce_fwd_mx4")
     D = int(D)
-    T = _mx4_rows(a, hidden_codes, hidden_scales, D, name="hidden_")
-    V = _mx4_rows(a, embed_codes, embed_scales, D, name="embed_")
-    a(target, "target", (torch.int32,), numel=T)
-    a(score_mask, "score_mask", _MASK, numel=T, optional=True)
-    a(nats, "nats", (torch.float32,), numel=T)
-    a(lse, "lse", (torch.float32,), numel=T, optional=True)
+    T = _mx4_rows(a, hidden_codes, hidden_scales, D, None, "hidden_codes", "hidden_scales")
+    V = _mx4_rows(a, embed_codes, embed_scales, D, None, "embed_codes", "embed_scales")
+    a(target, "target", _I32, T)
+    if score_mask is not None:
+        a(score_mask, "score_mask", _MASK, T)
+    a(nats, "nats", _F32, T)
+    if lse is not None:
+        a(lse, "lse", _F32, T)
     ws = _workspace(a, PG_OP_FWD_MX4, T, D, V, embed_codes, workspace)
     _enqueue(a.where, embed_codes, stream, _ptr(hidden_codes), _ptr(hidden_scales), _ptr(embed_codes),
              _ptr(embed_scales), _ptr(target), _ptr(score_mask), T, D, V, float(softcap), _ptr(nats), _ptr(lse),
