@@ -26,6 +26,7 @@ struct FwdMx4Params {
   int grid;               // workgroups that share rows and splits
   int rows_per_wg;
   int splits;             // of the vocabulary; 0: from the row count and the grid
+  int per;                // tiles of a split, where the host chose the splits
   Softcap sc;
   float* nats;
   float* lse;
@@ -34,14 +35,14 @@ struct FwdMx4Params {
   float* s_target;
 };
 
-// Vocabulary splits where only the device knows the row count: as many as the grid has workgroups for each
-// row tile, at most one per tile of the vocabulary.
+// Vocabulary splits: the host's choice, or, where only the device knows the row count, as many as the grid
+// has workgroups for each row tile, at most one per tile of the vocabulary. (n < 2^31: 32-bit divisions.)
 __host__ __device__ __forceinline__ int mx4_splits(const FwdMx4Params& p, int64_t n, int ntiles) {
   if (p.splits > 0) return p.splits;
-  const int64_t rt = (n + p.rows_per_wg - 1) / p.rows_per_wg;
-  if (rt <= 0) return 1;
-  const int64_t s = p.grid / rt;
-  return s < 1 ? 1 : (s > ntiles ? ntiles : (int)s);
+  const uint32_t rt = ((uint32_t)n + (uint32_t)p.rows_per_wg - 1u) / (uint32_t)p.rows_per_wg;
+  if (rt == 0u) return 1;
+  const uint32_t s = (uint32_t)p.grid / rt;
+  return s < 1u ? 1 : (s > (uint32_t)ntiles ? ntiles : (int)s);
 }
 
 // The target's term is one of the sum's, so a negative difference is a rounding (NaN passes).
@@ -218,11 +219,19 @@ __global__ __launch_bounds__(512, KS <= 8 && RB == 1 ? 4 : 2) void fwd_mx4_kerne
   const int h = lane >> 5, col = lane & 31;
   const int64_t n = p.n_dev ? (int64_t)(*p.n_dev) : p.n_host;
   const int ntiles = (p.V + TL::kRows - 1) / TL::kRows;
-  const int S = mx4_splits(p, n, ntiles);
-  const int64_t rt = blockIdx.x / S;
-  const int split = blockIdx.x % S;
+  // the host's choice comes as a grid of splits x row tiles (row tiles alone for one split): no divisions
+  int S = p.splits, per = p.per, split = 0;
+  int64_t rt = blockIdx.x;
+  if (S == 0) {
+    S = mx4_splits(p, n, ntiles);
+    rt = blockIdx.x / (uint32_t)S;
+    split = blockIdx.x % (uint32_t)S;
+    per = (ntiles + S - 1) / S;
+  } else if (S > 1) {
+    rt = blockIdx.y;
+    split = blockIdx.x;
+  }
   if (rt * (128 * RB) >= n) return;
-  const int per = (ntiles + S - 1) / S;
   const int t0 = split * per, t1 = min(t0 + per, ntiles);
 
   // This wave's part of a tile: kLoads pieces of codes (piece j: 1 KiB, lane i its 16 bytes at 16 i), and
@@ -531,52 +540,59 @@ __global__ __launch_bounds__(512, KS <= 8 && RB == 1 ? 4 : 2) void fwd_mx4_kerne
   }
 }
 
-// The splits' sums of each scored row, in split order. tile: vocabulary rows of a tile, which the
-// splits count. One split has written its rows itself where `direct` says so.
+// The splits' sums of each scored row: 16 lanes take four splits at a time each, then their sums are added in a
+// fixed order. tile: vocabulary rows of a tile, which the splits count. One split has written its rows itself
+// where `direct` says so.
+constexpr int kMx4FinalLanes = 16, kMx4FinalRows = 256 / kMx4FinalLanes;
 __global__ __launch_bounds__(256) void fwd_mx4_finalize_kernel(FwdMx4Params p, int tile, int fixed, int direct) {
   const int64_t n = p.n_dev ? (int64_t)(*p.n_dev) : p.n_host;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
   const int S = mx4_splits(p, n, (p.V + tile - 1) / tile);
   if (direct && S == 1) return;
-  const int64_t r = p.rows ? (int64_t)p.rows[i] : i;
-  const int stride = mx4_split_stride(S);
-  const float* pl = p.part_l + i * stride;
-  const float* pm = p.part_m + i * stride;
-  const float sy = p.s_target[i];
-  float m = p.sc.M, l = 0.f;   // M is the fixed shift's reference
-  if (!fixed) m = -INFINITY;
-  // eight splits at a time, so that their loads' latencies overlap
-  int s = 0;
-  for (; s + 8 <= S; s += 8) {
-    const float4 l0 = *reinterpret_cast<const float4*>(pl + s), l1 = *reinterpret_cast<const float4*>(pl + s + 4);
-    if (fixed) {
-      l += ((l0.x + l0.y) + (l0.z + l0.w)) + ((l1.x + l1.y) + (l1.z + l1.w));
-    } else {
-      const float4 m0 = *reinterpret_cast<const float4*>(pm + s), m1 = *reinterpret_cast<const float4*>(pm + s + 4);
-      lse_merge(m, l, m0.x, l0.x);
-      lse_merge(m, l, m0.y, l0.y);
-      lse_merge(m, l, m0.z, l0.z);
-      lse_merge(m, l, m0.w, l0.w);
-      lse_merge(m, l, m1.x, l1.x);
-      lse_merge(m, l, m1.y, l1.y);
-      lse_merge(m, l, m1.z, l1.z);
-      lse_merge(m, l, m1.w, l1.w);
+  const int stride = mx4_split_stride(S), lane = threadIdx.x % kMx4FinalLanes;
+  for (int64_t i = (int64_t)blockIdx.x * kMx4FinalRows + threadIdx.x / kMx4FinalLanes; i < n;
+       i += (int64_t)gridDim.x * kMx4FinalRows) {
+    const float* pl = p.part_l + i * stride;
+    const float* pm = p.part_m + i * stride;
+    const float sy = p.s_target[i];
+    const int64_t r = p.rows ? (int64_t)p.rows[i] : i;
+    float m = fixed ? p.sc.M : -INFINITY, l = 0.f;   // M is the fixed shift's reference
+    for (int s = 4 * lane; s < S; s += 4 * kMx4FinalLanes) {
+      if (s + 4 <= S) {
+        const float4 v = *reinterpret_cast<const float4*>(pl + s);
+        if (fixed) {
+          l += (v.x + v.y) + (v.z + v.w);
+        } else {
+          const float4 u = *reinterpret_cast<const float4*>(pm + s);
+          lse_merge(m, l, u.x, v.x);
+          lse_merge(m, l, u.y, v.y);
+          lse_merge(m, l, u.z, v.z);
+          lse_merge(m, l, u.w, v.w);
+        }
+      } else {   // the last splits, fewer than four
+        for (int e = s; e < S; ++e) {
+          if (fixed) l += pl[e];
+          else lse_merge(m, l, pm[e], pl[e]);
+        }
+      }
     }
+    if (fixed) {
+      l = group_sum<kMx4FinalLanes>(l);
+    } else {
+#pragma unroll
+      for (int off = 1; off < kMx4FinalLanes; off <<= 1) lse_merge(m, l, __shfl_xor(m, off), __shfl_xor(l, off));
+    }
+    if (lane != 0) continue;
+    p.nats[r] = kLn2 * (fixed ? log2_ratio(l, sy) : not_below_zero(m + flog2(l) - sy));
+    if (p.lse) p.lse[r] = kLn2 * (m + flog2(l));
   }
-  for (; s < S; ++s) {
-    if (fixed) l += pl[s];
-    else lse_merge(m, l, pm[s], pl[s]);
-  }
-  p.nats[r] = kLn2 * (fixed ? log2_ratio(l, sy) : not_below_zero(m + flog2(l) - sy));
-  if (p.lse) p.lse[r] = kLn2 * (m + flog2(l));
 }
 
 template <int KS, int RB>
 static void launch_fwd_mx4_rb(const FwdMx4Params& p, hipStream_t st) {
-  if (p.sc.fixed) hipLaunchKernelGGL((fwd_mx4_kernel<KS, RB, kMx4Fixed>), dim3(p.grid), dim3(512), 0, st, p);
-  else if (p.sc.c > 0.f) hipLaunchKernelGGL((fwd_mx4_kernel<KS, RB, kMx4Capped>), dim3(p.grid), dim3(512), 0, st, p);
-  else hipLaunchKernelGGL((fwd_mx4_kernel<KS, RB, kMx4Uncapped>), dim3(p.grid), dim3(512), 0, st, p);
+  const dim3 grid = p.splits > 1 ? dim3(p.splits, p.grid / p.splits) : dim3(p.grid);
+  if (p.sc.fixed) hipLaunchKernelGGL((fwd_mx4_kernel<KS, RB, kMx4Fixed>), grid, dim3(512), 0, st, p);
+  else if (p.sc.c > 0.f) hipLaunchKernelGGL((fwd_mx4_kernel<KS, RB, kMx4Capped>), grid, dim3(512), 0, st, p);
+  else hipLaunchKernelGGL((fwd_mx4_kernel<KS, RB, kMx4Uncapped>), grid, dim3(512), 0, st, p);
 }
 
 template <int KS>
@@ -642,7 +658,8 @@ hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const u
           p.splits = S;
         }
       }
-      p.grid = (int)(rt * p.splits);
+      p.per = (ntiles + p.splits - 1) / p.splits;
+      p.grid = (int)(rt * p.splits);   // several splits: at most 2^11 row tiles
     }
     fixed = p.sc.fixed;
     direct = 1;
@@ -670,8 +687,8 @@ hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const u
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (direct && !mask && mx4_splits(p, T, (V + tile - 1) / tile) == 1) return hipSuccess;
-  hipLaunchKernelGGL(fwd_mx4_finalize_kernel, dim3((unsigned)((T + 255) / 256)), dim3(256), 0, st, p, tile, fixed,
-                     direct);
+  hipLaunchKernelGGL(fwd_mx4_finalize_kernel, dim3(resident_blocks(dev, T, kMx4FinalRows)), dim3(256), 0, st, p, tile,
+                     fixed, direct);
   return hipGetLastError();
 }
 
