@@ -23,7 +23,8 @@ struct FwdMx4Params {
   int steps;              // 64-value steps of a row
   int V;
   int nblocks;            // 32-row blocks of the vocabulary
-  int grid;               // workgroups that share rows and splits
+  int grid;               // workgroups of the launch
+  int aim;                // workgroups that splits make of few rows
   int rows_per_wg;
   int splits;             // of the vocabulary; 0: from the row count and the grid
   int per;                // tiles of a split, where the host chose the splits
@@ -35,13 +36,13 @@ struct FwdMx4Params {
   float* s_target;
 };
 
-// Vocabulary splits: the host's choice, or, where only the device knows the row count, as many as the grid
-// has workgroups for each row tile, at most one per tile of the vocabulary. (n < 2^31: 32-bit divisions.)
+// Vocabulary splits: the host's choice, or, where only the device knows the row count, as many as make `aim`
+// workgroups, at most one per tile of the vocabulary. (n < 2^31: 32-bit divisions.)
 __host__ __device__ __forceinline__ int mx4_splits(const FwdMx4Params& p, int64_t n, int ntiles) {
   if (p.splits > 0) return p.splits;
   const uint32_t rt = ((uint32_t)n + (uint32_t)p.rows_per_wg - 1u) / (uint32_t)p.rows_per_wg;
   if (rt == 0u) return 1;
-  const uint32_t s = (uint32_t)p.grid / rt;
+  const uint32_t s = (uint32_t)p.aim / rt;
   return s < 1u ? 1 : (s > (uint32_t)ntiles ? ntiles : (int)s);
 }
 
@@ -639,20 +640,28 @@ hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const u
   int tile = 32, fixed = 0, direct = 0;
   p.rows_per_wg = 128;
   if (p.steps <= 16) {
-    if (p.steps <= 8 && !mask && T >= (int64_t)256 * ncu) p.rows_per_wg = 256;
+    const bool wide = p.steps <= 8 && !mask && T >= (int64_t)256 * ncu;
+    if (wide) p.rows_per_wg = 256;
     const int64_t rt = (T + p.rows_per_wg - 1) / p.rows_per_wg;
-    int64_t slots = p.rows_per_wg == 256 ? ncu : 2 * ncu;   // workgroups that run at once
+    int64_t slots = wide ? ncu : 2 * ncu;   // workgroups that run at once
     if (slots > 1024) slots = 1024;
-    p.grid = (int)(rt > slots ? rt : slots);
+    // where only the device knows the row count: one workgroup per CU (two that share it take as long, and
+    // twice the splits are merged: 2048 rows 16.0 against 17.6 us)
+    p.aim = ncu < 1024 ? ncu : 1024;
+    p.grid = (int)(rt > p.aim ? rt : p.aim);
     if (!mask) {
-      // the split with the fewest tiles one after another: rounds of workgroups times the tiles of each
-      // (and about one more that its start costs), within the partial sums' room
+      // The split that is done first, counted in hundredths of a tile's time on a CU that two workgroups
+      // share: rounds of workgroups times the tiles of each and about one more that a start costs; a last
+      // round of one workgroup per CU takes little more than half (one that owns its CU alone, of 64 rows per
+      // wave, has no such sharing); merging the splits costs about three. Within the partial sums' room.
       const int ntiles = p.steps <= 8 ? (V + Mx4Tile<8>::kRows - 1) / Mx4Tile<8>::kRows
                                       : (V + Mx4Tile<16>::kRows - 1) / Mx4Tile<16>::kRows;
       int64_t best = INT64_MAX;
       for (int S = 1; S <= ntiles && S <= 64; ++S) {
         if (S > 1 && T * mx4_split_stride(S) > fwd_partial_entries(T)) break;
-        const int64_t rounds = (rt * S + slots - 1) / slots, cost = rounds * ((ntiles + S - 1) / S + 1);
+        const int64_t wgs = rt * S, rounds = wgs / slots, rest = wgs % slots;
+        const int64_t each = (ntiles + S - 1) / S + 1;
+        const int64_t cost = (rounds * 100 + (rest == 0 ? 0 : !wide && rest <= ncu ? 55 : 100)) * each + (S > 1 ? 300 : 0);
         if (cost < best) {
           best = cost;
           p.splits = S;
@@ -681,7 +690,8 @@ hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const u
     }
   } else {
     const int64_t rt = (T + 127) / 128;
-    p.grid = (int)(rt > 1024 ? rt : 1024);
+    p.aim = 1024;
+    p.grid = (int)(rt > p.aim ? rt : p.aim);
     hipLaunchKernelGGL(fwd_mx4_stream_kernel, dim3(p.grid), dim3(256), 0, st, p);
   }
   hipError_t e = hipGetLastError();
