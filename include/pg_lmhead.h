@@ -27,6 +27,8 @@
  *     the last such call's contents.
  *   - Every call is asynchronous on `stream` (a hipStream_t; NULL = the default stream) and never
  *     synchronises the host. Buffers must stay alive until the stream's work is done.
+ *   - A workspace belongs to one call at a time: calls that may overlap (on several streams, or from
+ *     captured graphs that are replayed side by side) need one each.
  *   - Arguments are validated on the host before anything is launched; a non-zero status means
  *     nothing was enqueued. Data errors found on the device (a target outside [0, V) on a scored
  *     row, NaN/Inf inputs) are not reported as codes: they turn the affected nats into NaN, which

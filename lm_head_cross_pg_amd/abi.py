@@ -462,6 +462,15 @@ def _enqueue(entry: str, ref: torch.Tensor, stream, *args) -> None:
         _check(status, entry)
 
 
+def _scratch(a: _Args, op: int, T: int, D: int, V: int, ref: torch.Tensor, workspace, stream):
+    """The caller's workspace, or one of its own for the call. One of its own that a stream other than the
+    current one works on is not reused before that stream is done with it."""
+    ws = _workspace(a, op, T, D, V, ref, workspace)
+    if workspace is None and stream is not None and int(stream) != _raw_stream(ref.get_device()):
+        ws.record_stream(torch.cuda.ExternalStream(int(stream), device=ref.device))
+    return ws
+
+
 def _norm_inputs(a: _Args, x, weight, bias, score_mask):
     """x [T, D] bf16 or float32, weight and bias float32 [D] or None, score_mask uint8/bool [T] or None."""
     T, D = _matrix(a, x, "x", _FLOATS)
@@ -535,7 +544,7 @@ def pg_layernorm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], score_mask
     a(dx, "dx", _FLOATS, shape=(T, D), optional=True)
     a(dweight, "dweight", (torch.float32,), numel=D, optional=True)
     a(dbias, "dbias", (torch.float32,), numel=D, optional=True)
-    ws = _workspace(a, PG_OP_LN_BWD, T, D, 1, x, workspace)
+    ws = _scratch(a, PG_OP_LN_BWD, T, D, 1, x, workspace, stream)
     _enqueue(a.where, x, stream, _ptr(x), _dtype_code(x), _ptr(weight), _ptr(score_mask), _ptr(dy), _dtype_code(dy),
              T, D, float(eps), _ptr(dx), PG_DTYPE_F32 if dx is None else _dtype_code(dx), _ptr(dweight),
              _ptr(dbias), _ptr(ws), ws.numel())
@@ -573,7 +582,7 @@ def pg_lmhead_ce_fwd_mx4(hidden_codes: torch.Tensor, hidden_scales: torch.Tensor
     a(nats, "nats", _F32, T)
     if lse is not None:
         a(lse, "lse", _F32, T)
-    ws = _workspace(a, PG_OP_FWD_MX4, T, D, V, embed_codes, workspace)
+    ws = _scratch(a, PG_OP_FWD_MX4, T, D, V, embed_codes, workspace, stream)
     _enqueue(a.where, embed_codes, stream, _ptr(hidden_codes), _ptr(hidden_scales), _ptr(embed_codes),
              _ptr(embed_scales), _ptr(target), _ptr(score_mask), T, D, V, float(softcap), _ptr(nats), _ptr(lse),
              _ptr(ws), ws.numel())

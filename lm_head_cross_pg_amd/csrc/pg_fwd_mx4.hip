@@ -657,7 +657,7 @@ hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const u
       const int ntiles = p.steps <= 8 ? (V + Mx4Tile<8>::kRows - 1) / Mx4Tile<8>::kRows
                                       : (V + Mx4Tile<16>::kRows - 1) / Mx4Tile<16>::kRows;
       int64_t best = INT64_MAX;
-      for (int S = 1; S <= ntiles && S <= 64; ++S) {
+      for (int S = 1; S <= ntiles && S <= slots; S += S < 64 ? 1 : S) {   // every one up to 64, then powers of two
         if (S > 1 && T * mx4_split_stride(S) > fwd_partial_entries(T)) break;
         const int64_t wgs = rt * S, rounds = wgs / slots, rest = wgs % slots;
         const int64_t each = (ntiles + S - 1) / S + 1;

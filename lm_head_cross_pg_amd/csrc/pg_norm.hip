@@ -506,14 +506,38 @@ __global__ __launch_bounds__(kNormSumThreads) void norm_bwd_sum_kernel(const flo
   }
 }
 
-constexpr int kNormBwdBlocks = 256;     // workgroups of the backward, and partial sums: one per CU
+// Workgroups of the backward, and partial sums: one per CU, and more where a lane would add over
+// kNormLaneRows rows in float32 (the partial sums are added in float64).
+constexpr int kNormBwdBlocks = 256;
+constexpr int64_t kNormLaneRows = 512;
 constexpr int kNormColumnRows = 64;     // rows of T that split the column sums of wide rows, at most
+
+// The backward's launch for rows that waves hold: lanes per row, chunks per lane, waves per workgroup (four
+// where that keeps every workgroup at work, up to the most where rows are many), workgroups.
+struct NormBwdLaunch {
+  int lpr, chunks, waves, blocks;
+};
+static NormBwdLaunch norm_bwd_launch(int64_t T, int32_t D) {
+  NormBwdLaunch L;
+  L.lpr = D <= 128 ? 16 : D <= 256 ? 32 : 64;
+  L.chunks = D <= 512 ? 1 : D <= 1024 ? 2 : 4;
+  const int most = L.chunks == 1 ? NormBwdShape<1>::kThreads / 64
+                                 : L.chunks == 2 ? NormBwdShape<2>::kThreads / 64 : NormBwdShape<4>::kThreads / 64;
+  const int64_t rows = (T + 64 / L.lpr - 1) / (64 / L.lpr);   // per wave, side by side
+  L.waves = 4;
+  while (L.waves < most && rows > (int64_t)L.waves * kNormBwdBlocks) L.waves *= 2;
+  const int64_t need = (rows + L.waves - 1) / L.waves;
+  const int64_t cap = (need + kNormLaneRows - 1) / kNormLaneRows;
+  const int64_t most_blocks = cap > kNormBwdBlocks ? cap : kNormBwdBlocks;
+  L.blocks = (int)(need < most_blocks ? need : most_blocks);
+  return L;
+}
 
 NormBwdWorkspace norm_bwd_workspace(int64_t T, int32_t D) {
   NormBwdWorkspace L;
   const bool wide = D > kRowWaveMax;
   L.part = 0;
-  L.stats = align256((size_t)(wide ? kNormColumnRows : kNormBwdBlocks) * 2 * (size_t)D * 4);
+  L.stats = align256((size_t)(wide ? kNormColumnRows : norm_bwd_launch(T, D).blocks) * 2 * (size_t)D * 4);
   L.total = L.stats + (wide ? align256((size_t)T * 16) : 0);
   return L;
 }
@@ -530,21 +554,15 @@ static void launch_norm_bwd_t(const NormBwdParams& p, int& blocks, hipStream_t s
     }
     return;
   }
-#define PG_NORM_BWD(LPR, K)                                                                                      \
-  {                                                                                                              \
-    /* waves of a workgroup: four where that keeps every workgroup at work, up to the most where rows are many */ \
-    const int64_t rows = (p.T + 64 / LPR - 1) / (64 / LPR);                                                       \
-    int waves = 4;                                                                                                \
-    while (waves < NormBwdShape<K>::kThreads / 64 && rows > (int64_t)waves * kNormBwdBlocks) waves *= 2;          \
-    const int64_t need = (rows + waves - 1) / waves;                                                              \
-    blocks = (int)(need < kNormBwdBlocks ? need : kNormBwdBlocks);                                                \
-    hipLaunchKernelGGL((norm_bwd_rows_kernel<TX, TDY, TDX, LPR, K>), dim3(blocks), dim3(64 * waves), 0, st, p);   \
-  }
-  if (D <= 128) PG_NORM_BWD(16, 1)
-  else if (D <= 256) PG_NORM_BWD(32, 1)
-  else if (D <= 512) PG_NORM_BWD(64, 1)
-  else if (D <= 1024) PG_NORM_BWD(64, 2)
-  else PG_NORM_BWD(64, 4)
+  const NormBwdLaunch L = norm_bwd_launch(p.T, D);
+  blocks = L.blocks;
+#define PG_NORM_BWD(LPR, K) \
+  hipLaunchKernelGGL((norm_bwd_rows_kernel<TX, TDY, TDX, LPR, K>), dim3(blocks), dim3(64 * L.waves), 0, st, p)
+  if (L.lpr == 16) PG_NORM_BWD(16, 1);
+  else if (L.lpr == 32) PG_NORM_BWD(32, 1);
+  else if (L.chunks == 1) PG_NORM_BWD(64, 1);
+  else if (L.chunks == 2) PG_NORM_BWD(64, 2);
+  else PG_NORM_BWD(64, 4);
 #undef PG_NORM_BWD
 }
 

@@ -351,3 +351,62 @@ def test_repeatable_on_another_stream_and_in_a_graph():
             assert all(torch.equal(a, b) for a, b in zip(first, (nats, lse, out)))
             step()
             torch.cuda.synchronize()
+
+
+def test_two_calls_at_once():
+    """The head on two streams with nothing between them, one workspace given and one allocated by the call:
+    the bits of the calls one by one."""
+    T, D, V = 3000, 512, 2000
+    ins = [head_inputs(T, D, V, s, 4.0) for s in (30, 31)]
+    ys = [i[2].cuda() for i in ins]
+    torch.cuda.synchronize()
+
+    def run(i, stream, ws):
+        nats, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(5):
+            abi.pg_lmhead_ce_fwd_mx4(*ins[i][0], *ins[i][1], ys[i], None, D, 30.0, nats, lse, ws, stream=stream)
+        return nats, lse
+
+    want = [run(0, None, None), run(1, None, None)]
+    s0, s1 = torch.cuda.Stream(), torch.cuda.Stream()
+    ws = torch.empty(abi.workspace_bytes(abi.PG_OP_FWD_MX4, T, D, V), dtype=torch.uint8, device="cuda")
+    got = [run(0, s0.cuda_stream, ws), run(1, s1.cuda_stream, None)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_rows_past_32_bit_offsets():
+    """9 x 10^6 rows (2.3 x 10^9 bytes of codes, 4.6 x 10^9 values): quantised, read back and scored, the last
+    rows as in calls on them alone."""
+    T, D, V, K = 9_000_000, 512, 96, 200
+    x = torch.empty((T, D), dtype=BF, device="cuda")
+    x[:T - K] = 0.5
+    x[T - K:] = rows(K, D, BF, 40).cuda()
+    codes, scales = (torch.empty((T, n), dtype=torch.uint8, device="cuda") for n in (256, 16))
+    abi.pg_quantize_mx4(x, None, codes, scales)
+    sc, ss = room(K, D)
+    abi.pg_quantize_mx4(x[T - K:].contiguous(), None, sc, ss)
+    assert torch.equal(codes[T - K:], sc) and torch.equal(scales[T - K:], ss)
+    abi.pg_dequantize_mx4(codes, scales, x)
+    out = torch.empty((K, D), dtype=BF, device="cuda")
+    abi.pg_dequantize_mx4(sc, ss, out)
+    assert torch.equal(x[T - K:], out) and bool((x[0] == 0.5).all())
+    del x
+    _, eq, _, _, _ = head_inputs(1, D, V, 41)
+    y = torch.zeros(T, dtype=torch.int32, device="cuda")
+    nats = torch.empty(T, device="cuda")
+    abi.pg_lmhead_ce_fwd_mx4(codes, scales, *eq, y, None, D, 30.0, nats)
+    small = torch.empty(K, device="cuda")
+    abi.pg_lmhead_ce_fwd_mx4(sc, ss, *eq, y[:K].contiguous(), None, D, 30.0, small)
+    # one split either way (one tile of vocabulary): the same operations on each row
+    assert torch.equal(nats[T - K:], small)
+
+
+def test_head_widest_vocabulary_and_states():
+    """V = 2^20 for few rows (the splits go past 64), and D = 2^16."""
+    check_head(3, 32, 1 << 20, 30.0, 50)
+    check_head(5, 1 << 16, 70, 30.0, 51)
+    mask = torch.tensor([1, 0, 1, 1, 0], dtype=torch.uint8)
+    check_head(5, 64, 1 << 18, 0.0, 52, mask=mask)

@@ -278,3 +278,76 @@ def test_repeatable_on_another_stream_and_in_a_graph():
         assert all(torch.equal(a, b) for a, b in zip(first, (y, dx, dw, db)))
         step()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("D", [96, 512, 2600])
+def test_two_calls_at_once(D):
+    """Forward and backward on two streams with nothing between them, workspaces of their own (one given, one
+    allocated by the call on a stream that is not the current one): the bits of the calls one by one."""
+    T = 4000
+    ins = []
+    for seed in (20, 21):
+        x, w, b = states(T, D, BF, seed)
+        ins.append(cuda(x, w, b, gradients(T, D, F, seed)))
+
+    def run(i, stream, ws):
+        x, w, b, dy = ins[i]
+        out = [torch.empty((T, D), device="cuda"), torch.empty((T, D), device="cuda"), torch.empty(D, device="cuda"),
+               torch.empty(D, device="cuda")]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            abi.pg_layernorm_fwd(x, w, b, None, 1e-5, out[0], stream=stream)
+            abi.pg_layernorm_bwd(x, w, None, dy, 1e-5, *out[1:], ws, stream=stream)
+        return out
+
+    want = [run(0, None, None), run(1, None, None)]
+    torch.cuda.synchronize()
+    want = [[t.clone() for t in o] for o in want]
+    s0, s1 = torch.cuda.Stream(), torch.cuda.Stream()
+    ws = torch.empty(abi.workspace_bytes(abi.PG_OP_LN_BWD, T, D, 1), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    got = [run(0, s0.cuda_stream, ws), run(1, s1.cuda_stream, None)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_rows_past_32_bit_offsets():
+    """2.3 x 10^9 values: the last rows of the forward and the backward are those of a call on them alone, and
+    dw, db of a mask that leaves only them too."""
+    T, D, K = 4_500_000, 512, 96
+    x = torch.empty((T, D), dtype=BF, device="cuda")
+    x[:T - K] = 1.0
+    tail, w, b = states(K, D, BF, 22)
+    x[T - K:] = tail.cuda()
+    w, b = w.cuda(), b.cuda()
+    dy = torch.zeros((T, D), dtype=BF, device="cuda")
+    dy[T - K:] = gradients(K, D, BF, 22).cuda()
+    y = torch.empty_like(x)
+    abi.pg_layernorm_fwd(x, w, b, None, 1e-5, y)
+    small = torch.empty((K, D), dtype=BF, device="cuda")
+    abi.pg_layernorm_fwd(x[T - K:].contiguous(), w, b, None, 1e-5, small)
+    assert torch.equal(y[T - K:], small) and torch.equal(y[0], b.to(BF))
+    del y
+    mask = torch.zeros(T, dtype=torch.uint8, device="cuda")
+    mask[T - K:] = 1
+    dx, dw, db = torch.empty_like(x), torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    abi.pg_layernorm_bwd(x, w, mask, dy, 1e-5, dx, dw, db)
+    sdx, sdw, sdb = torch.empty((K, D), dtype=BF, device="cuda"), torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    abi.pg_layernorm_bwd(x[T - K:].contiguous(), w, None, dy[T - K:].contiguous(), 1e-5, sdx, sdw, sdb)
+    assert torch.equal(dx[T - K:], sdx) and not dx[:T - K].any()
+    # the rows fall to other lanes: each adds at most one of them here and there, the rest in float64
+    mag = dy[T - K:].double().abs().sum(0)
+    assert float(((db - sdb).double().abs() - 2 * U * db.double().abs() - 40 * U * mag).max()) <= 0
+
+
+def test_many_rows_keep_the_sums_digits():
+    """2^23 rows of equal sign: db is a sum of equal values, whose float32 running sum alone would be off by
+    far more than the (512 + 24) u that lanes of at most 512 rows allow."""
+    T, D = 1 << 23, 16
+    x = torch.randn((T, D), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").to(BF)
+    dy = torch.full((T, D), 0.1, device="cuda")
+    dw, db = torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    abi.pg_layernorm_bwd(x, None, None, dy, 1e-5, None, dw, db)
+    want = T * float(torch.tensor(0.1))
+    assert float((db.double() - want).abs().max()) <= (512 + 24) * U * want
