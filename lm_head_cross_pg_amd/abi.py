@@ -177,7 +177,10 @@ class _Args:
 
     def same_device(self):
         index = self.seen[0][1].get_device()   # negative off the GPU
-        if index >= 0 and all(t.get_device() == index for _, t in self.seen):
+        for _, t in self.seen:
+            if t.get_device() != index or index < 0:
+                break
+        else:
             return
         dev = None
         for name, t in self.seen:
@@ -445,15 +448,16 @@ _FLOATS = _BF16 + (torch.float32,)
 # time of making a Stream object, which is a quarter of a small call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _enqueue(entry: str, ref: torch.Tensor, stream, *args) -> None:
     """The library call on the device that holds the tensors, whichever is current: on `stream`, or
     on that device's current one."""
-    fn = getattr(load(), entry)
+    fn = getattr(_lib or load(), entry)
     index = ref.get_device()
     stream = _raw_stream(index) if stream is None else int(stream)
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, stream)
     else:
         with torch.cuda.device(index):
