@@ -49,6 +49,20 @@ __device__ __forceinline__ uint32_t mx4_encode8(const float* v, float scale) {
   return o;
 }
 
+// What eight codes stand for, exactly (checked for every code at every scale byte but NaN's).
+__device__ __forceinline__ void mx4_decode8(uint32_t w, float scale, float* v) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 1);
+  const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 3);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    v[j] = a[j];
+    v[2 + j] = b[j];
+    v[4 + j] = c[j];
+    v[6 + j] = d[j];
+  }
+}
+
 // Lane c of a row's lanes holds chunk c (values 8 c .. 8 c + 7, zeros past D) in v: the four lanes of
 // a block agree on its scale, each stores its four bytes of codes, and the first of 16 the four scale
 // bytes of its blocks as one word (after the row's last, the zeros up to the padded end). Every lane of

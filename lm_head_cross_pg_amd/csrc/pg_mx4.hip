@@ -42,15 +42,12 @@ __global__ __launch_bounds__(256) void dequantize_mx4_kernel(const uint8_t* code
   for (int64_t t = first; t < T; t += (int64_t)gridDim.x * 4 * RPW) {
     for (int c = l; c < nch; c += LPR) {
       const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + t * cb + 4 * (int64_t)c);
-      const float s = mx4_scale_value(scales[t * sb + (c >> 2)]);
+      const uint32_t byte = scales[t * sb + (c >> 2)];
       float v[8];
+      mx4_decode8(w, mx4_scale_value(byte), v);
+      if (byte == 255u) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t q = (w >> (4 * j)) & 15u;
-        // levels 0, 0.5, 1, 1.5 (codes 0 .. 3), then (2 + m) 2^(k - 1) for code 2 k + m, in halves
-        const uint32_t m = q & 7u, half = m < 4u ? m : (2u + (m & 1u)) << (((m >> 1) - 1u) & 3u);
-        const float a = 0.5f * (float)half;
-        v[j] = (q & 8u ? -a : a) * s;
+        for (int j = 0; j < 8; ++j) v[j] = __builtin_nanf("");
       }
       store_chunk(out + t * D, c, D, v);
     }

@@ -34,6 +34,10 @@ struct NormParams {
   uint8_t* scales;
 };
 
+// Rows that lanes hold in registers; the others (wider than a workgroup's registers, or less than a chunk) are
+// read anew for each pass.
+static bool row_held(int32_t D) { return D >= kRowChunkMin && D <= kRowGroupMax; }
+
 // The gain and bias of chunk c (ones and zeros where there are none).
 __device__ __forceinline__ void norm_params_chunk(const NormParams& p, int c, float* w, float* b) {
   if (p.weight) load_chunk(p.weight, c, p.D, w);
@@ -100,7 +104,10 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormParams p) {
   for (int64_t t = first; t < p.T; t += step) {
     float x[K][8];
 #pragma unroll
-    for (int k = 0; k < K; ++k) raw[k].unpack(x[k]);
+    for (int k = 0; k < K; ++k) {
+      if (!full) raw[k].place(l + k * LPR, p.D);
+      raw[k].unpack(x[k]);
+    }
     const bool now = scored;
     scored = fetch(t + step);
     if (!now) continue;
@@ -139,7 +146,61 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormParams p) {
   }
 }
 
-// Wider rows: a workgroup per row, which reads it three times (from L2 after the first).
+// Rows of up to kRowGroupMax: a workgroup holds a row, a chunk per lane (blockDim.x is 64 row_group_waves).
+template <typename TX, typename TOut>
+__global__ __launch_bounds__(64 * kRowGroupWaves) void norm_group_kernel(NormParams p) {
+  __shared__ double sh[2][kRowGroupWaves];
+  const int c = threadIdx.x, waves = blockDim.x >> 6;
+  const bool full = p.D == 8 * (int)blockDim.x;   // no lane has values past the row's end
+  double w[8], b[8];
+  {
+    float wf[8], bf[8];
+    norm_params_chunk(p, c, wf, bf);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w[j] = wf[j];
+      b[j] = bf[j];
+    }
+  }
+  // the row after this one is on its way while this one is worked on
+  RawChunk<TX> raw;
+  auto fetch = [&](int64_t t) {
+    const bool scored = t < p.T && !(p.mask && !p.mask[t]);
+    if (scored) raw.load(static_cast<const TX*>(p.x) + t * p.D, c, p.D);
+    return scored;
+  };
+  bool scored = fetch(blockIdx.x);
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+    float x[8];
+    if (!full) raw.place(c, p.D);
+    raw.unpack(x);
+    const bool now = scored;
+    scored = fetch(t + gridDim.x);
+    if (!now) continue;   // the same in every wave
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += (double)x[j];
+    put_wave_sum(s, sh[0]);
+    lds_barrier();
+    const double mean = wave_sums(sh[0], waves) * p.inv_d;
+    double d[8];
+    s = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      d[j] = 8 * c + j < p.D ? (double)x[j] - mean : 0.0;
+      s = __builtin_fma(d[j], d[j], s);
+    }
+    put_wave_sum(s, sh[1]);
+    lds_barrier();
+    const double r = rsqrt_f64(__builtin_fma(wave_sums(sh[1], waves), p.inv_d, p.eps));
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)__builtin_fma(d[j] * r, w[j], b[j]);
+    norm_store<TOut>(p, t, c, v);
+  }
+}
+
+// Other rows: a workgroup per row, which reads it three times (from L2 after the first).
 template <typename TX, typename TOut>
 __global__ __launch_bounds__(kRowThreads) void norm_wide_kernel(NormParams p) {
   __shared__ double sh[kRowThreads / 64];
@@ -175,11 +236,19 @@ __global__ __launch_bounds__(kRowThreads) void norm_wide_kernel(NormParams p) {
   }
 }
 
+constexpr int kGroupResident = 24;   // waves of norm_group_kernel that a CU holds at once
 template <typename TX, typename TOut>
 static void launch_norm_t(const NormParams& p, const DeviceInfo& dev, hipStream_t st) {
   const int D = p.D;
-  if (D > kRowWaveMax) {
+  if (!row_held(D)) {
     hipLaunchKernelGGL((norm_wide_kernel<TX, TOut>), dim3(stride_blocks(p.T, 1)), dim3(kRowThreads), 0, st, p);
+    return;
+  }
+  if (D > kRowWaveMax) {
+    const int waves = row_group_waves(D);
+    const int64_t most = (int64_t)kGroupResident / waves * dev.cu_count;
+    hipLaunchKernelGGL((norm_group_kernel<TX, TOut>), dim3((unsigned)(p.T < most ? p.T : most)), dim3(64 * waves), 0,
+                       st, p);
     return;
   }
 #define PG_NORM(LPR, K)                                                                                          \
@@ -188,8 +257,7 @@ static void launch_norm_t(const NormParams& p, const DeviceInfo& dev, hipStream_
   if (D <= 128) PG_NORM(16, 1);
   else if (D <= 256) PG_NORM(32, 1);
   else if (D <= 512) PG_NORM(64, 1);
-  else if (D <= 1024) PG_NORM(64, 2);
-  else PG_NORM(64, 4);
+  else PG_NORM(64, 2);
 #undef PG_NORM
 }
 
@@ -255,7 +323,7 @@ struct NormBwdParams {
 template <int K>
 struct NormBwdShape {
   // threads of a workgroup, at most: as many waves as share one partial sum, within the registers they need
-  static constexpr int kThreads = K == 1 ? 1024 : K == 2 ? 512 : 256;
+  static constexpr int kThreads = K == 1 ? 1024 : 512;
 };
 
 template <typename TX, typename TDY, typename TDX, int LPR, int K>
@@ -263,6 +331,7 @@ __global__ __launch_bounds__(NormBwdShape<K>::kThreads) void norm_bwd_rows_kerne
   constexpr int RPW = 64 / LPR;
   __shared__ float sums[2][LPR * K * 8];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, l = lane % LPR;
+  const bool full = p.D == LPR * K * 8;   // no lane has values past the row's end
   float w[K][8], dw[K][8], db[K][8];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -296,6 +365,10 @@ __global__ __launch_bounds__(NormBwdShape<K>::kThreads) void norm_bwd_rows_kerne
     float x[K][8], dy[K][8];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      if (!full) {
+        rx[k].place(l + k * LPR, p.D);
+        rdy[k].place(l + k * LPR, p.D);
+      }
       rx[k].unpack(x[k]);
       rdy[k].unpack(dy[k]);
     }
@@ -383,7 +456,88 @@ __global__ __launch_bounds__(NormBwdShape<K>::kThreads) void norm_bwd_rows_kerne
   }
 }
 
-// Wider rows: dx by a workgroup per row, the row's statistics kept for the column sums.
+// Rows of up to kRowGroupMax: a workgroup holds a row, a chunk per lane (blockDim.x is 64 row_group_waves),
+// and each lane the sums of its own eight columns.
+template <typename TX, typename TDY, typename TDX>
+__global__ __launch_bounds__(64 * kRowGroupWaves) void norm_bwd_group_kernel(NormBwdParams p) {
+  __shared__ double sh[2][kRowGroupWaves];
+  __shared__ float shf[2][kRowGroupWaves];
+  const int c = threadIdx.x, waves = blockDim.x >> 6;
+  const bool full = p.D == 8 * (int)blockDim.x;   // no lane has values past the row's end
+  float w[8], dw[8] = {}, db[8] = {};
+  if (p.weight) load_chunk(p.weight, c, p.D, w);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = p.weight ? w[j] : 1.f;
+  const float invD = (float)p.inv_d;
+  // the row after this one is on its way while this one is worked on
+  RawChunk<TX> rx;
+  RawChunk<TDY> rdy;
+  auto fetch = [&](int64_t t) {
+    const bool scored = t < p.T && !(p.mask && !p.mask[t]);
+    if (scored) {
+      rx.load(static_cast<const TX*>(p.x) + t * p.D, c, p.D);
+      rdy.load(static_cast<const TDY*>(p.dy) + t * p.D, c, p.D);
+    }
+    return scored;
+  };
+  bool scored = fetch(blockIdx.x);
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+    TDX* dxrow = static_cast<TDX*>(p.dx) + t * p.D;
+    float x[8], dy[8];
+    if (!full) {
+      rx.place(c, p.D);
+      rdy.place(c, p.D);
+    }
+    rx.unpack(x);
+    rdy.unpack(dy);
+    const bool now = scored;
+    scored = fetch(t + gridDim.x);
+    if (!now) {   // the same in every wave
+      const float zero[8] = {};
+      if (p.dx) store_chunk(dxrow, c, p.D, zero);
+      continue;
+    }
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += (double)x[j];
+    put_wave_sum(s, sh[0]);
+    lds_barrier();
+    const double mean = wave_sums(sh[0], waves) * p.inv_d;
+    float c1 = 0.f, c2 = 0.f;
+    s = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double d = 8 * c + j < p.D ? (double)x[j] - mean : 0.0;
+      s = __builtin_fma(d, d, s);
+      x[j] = (float)d;
+      const float g = dy[j] * w[j];
+      c1 += g;
+      c2 = __builtin_fmaf(g, x[j], c2);
+    }
+    put_wave_sum(s, sh[1]);
+    put_wave_sum(c1, shf[0]);
+    put_wave_sum(c2, shf[1]);
+    lds_barrier();
+    const float r = (float)rsqrt_f64(__builtin_fma(wave_sums(sh[1], waves), p.inv_d, p.eps));
+    c1 = wave_sums(shf[0], waves) * invD;
+    c2 = wave_sums(shf[1], waves) * r * invD;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float xh = x[j] * r;
+      dw[j] = __builtin_fmaf(dy[j], xh, dw[j]);
+      db[j] += dy[j];
+      v[j] = r * (__builtin_fmaf(dy[j], w[j], -c1) - xh * c2);
+    }
+    if (p.dx) store_chunk(dxrow, c, p.D, v);
+  }
+  if (!p.part) return;
+  float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
+  store_chunk(part, c, p.D, dw);
+  store_chunk(part + p.D, c, p.D, db);
+}
+
+// Other rows: dx by a workgroup per row, the row's statistics kept for the column sums.
 template <typename TX, typename TDY, typename TDX>
 __global__ __launch_bounds__(kRowThreads) void norm_bwd_wide_kernel(NormBwdParams p) {
   __shared__ double sh[kRowThreads / 64];
@@ -519,10 +673,17 @@ struct NormBwdLaunch {
 };
 static NormBwdLaunch norm_bwd_launch(int64_t T, int32_t D) {
   NormBwdLaunch L;
+  if (D > kRowWaveMax) {   // a workgroup per row, side by side on a CU while they are small
+    L.lpr = L.chunks = 0;
+    L.waves = row_group_waves(D);
+    const int64_t side = (T + kNormLaneRows - 1) / kNormLaneRows, least = kNormBwdBlocks * ((7 + L.waves) / L.waves);
+    const int64_t most = side > least ? side : least;
+    L.blocks = (int)(T < most ? T : most);
+    return L;
+  }
   L.lpr = D <= 128 ? 16 : D <= 256 ? 32 : 64;
-  L.chunks = D <= 512 ? 1 : D <= 1024 ? 2 : 4;
-  const int most = L.chunks == 1 ? NormBwdShape<1>::kThreads / 64
-                                 : L.chunks == 2 ? NormBwdShape<2>::kThreads / 64 : NormBwdShape<4>::kThreads / 64;
+  L.chunks = D <= 512 ? 1 : 2;
+  const int most = (L.chunks == 1 ? NormBwdShape<1>::kThreads : NormBwdShape<2>::kThreads) / 64;
   const int64_t rows = (T + 64 / L.lpr - 1) / (64 / L.lpr);   // per wave, side by side
   L.waves = 4;
   while (L.waves < most && rows > (int64_t)L.waves * kNormBwdBlocks) L.waves *= 2;
@@ -535,7 +696,7 @@ static NormBwdLaunch norm_bwd_launch(int64_t T, int32_t D) {
 
 NormBwdWorkspace norm_bwd_workspace(int64_t T, int32_t D) {
   NormBwdWorkspace L;
-  const bool wide = D > kRowWaveMax;
+  const bool wide = !row_held(D);
   L.part = 0;
   L.stats = align256((size_t)(wide ? kNormColumnRows : norm_bwd_launch(T, D).blocks) * 2 * (size_t)D * 4);
   L.total = L.stats + (wide ? align256((size_t)T * 16) : 0);
@@ -545,7 +706,7 @@ NormBwdWorkspace norm_bwd_workspace(int64_t T, int32_t D) {
 template <typename TX, typename TDY, typename TDX>
 static void launch_norm_bwd_t(const NormBwdParams& p, int& blocks, hipStream_t st) {
   const int D = p.D;
-  if (D > kRowWaveMax) {
+  if (!row_held(D)) {
     hipLaunchKernelGGL((norm_bwd_wide_kernel<TX, TDY, TDX>), dim3(stride_blocks(p.T, 1)), dim3(kRowThreads), 0, st, p);
     if (p.part) {
       blocks = (int)(p.T < kNormColumnRows ? p.T : kNormColumnRows);
@@ -558,11 +719,12 @@ static void launch_norm_bwd_t(const NormBwdParams& p, int& blocks, hipStream_t s
   blocks = L.blocks;
 #define PG_NORM_BWD(LPR, K) \
   hipLaunchKernelGGL((norm_bwd_rows_kernel<TX, TDY, TDX, LPR, K>), dim3(blocks), dim3(64 * L.waves), 0, st, p)
-  if (L.lpr == 16) PG_NORM_BWD(16, 1);
+  if (L.chunks == 0)
+    hipLaunchKernelGGL((norm_bwd_group_kernel<TX, TDY, TDX>), dim3(blocks), dim3(64 * L.waves), 0, st, p);
+  else if (L.lpr == 16) PG_NORM_BWD(16, 1);
   else if (L.lpr == 32) PG_NORM_BWD(32, 1);
   else if (L.chunks == 1) PG_NORM_BWD(64, 1);
-  else if (L.chunks == 2) PG_NORM_BWD(64, 2);
-  else PG_NORM_BWD(64, 4);
+  else PG_NORM_BWD(64, 2);
 #undef PG_NORM_BWD
 }
 

@@ -10,38 +10,91 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
-// Eight values of a row from element 8 c on, zeros past D. A whole chunk is one (bf16) or two (f32)
-// 16-byte loads, which need no more than the element's own alignment on this hardware: rows of any
-// width are read the same way.
-__device__ __forceinline__ void load_chunk(const float* row, int c, int D, float* v) {
-  if (8 * c + 8 <= D) {
-    const u32x4_a4 a = reinterpret_cast<const u32x4_a4*>(row + 8 * (int64_t)c)[0];
-    const u32x4_a4 b = reinterpret_cast<const u32x4_a4*>(row + 8 * (int64_t)c)[1];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = __uint_as_float(a[j]);
-      v[4 + j] = __uint_as_float(b[j]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 8 * c + j < D ? row[8 * (int64_t)c + j] : 0.f;
+// A chunk as it lies in memory, so that a load can be held in flight and unpacked when it is used: values
+// 8 c .. 8 c + 7, zeros past D. It is one (bf16) or two (f32) 16-byte loads, which need no more than the
+// element's own alignment on this hardware: rows of any width are read the same way. A chunk that the row's
+// end cuts off is read from D - 8 on and moved into place by `place`, before `unpack` (chunks wholly past the
+// end become zeros); nothing waits for a load before that. Rows of less than eight values are for load_chunk below.
+constexpr int kRowChunkMin = 8;
+__device__ __forceinline__ int chunk_start(int c, int D) { return 8 * c + 8 <= D ? 8 * c : D - 8; }
+
+template <typename T>
+struct RawChunk;
+template <>
+struct RawChunk<uint16_t> {
+  u32x4 a;
+  __device__ __forceinline__ void load(const uint16_t* row, int c, int D) {
+    a = *reinterpret_cast<const u32x4_a2*>(row + chunk_start(c, D));
   }
-}
-__device__ __forceinline__ void load_chunk(const uint16_t* row, int c, int D, float* v) {
-  if (8 * c + 8 <= D) {
-    const u32x4_a2 a = *reinterpret_cast<const u32x4_a2*>(row + 8 * (int64_t)c);
+  __device__ __forceinline__ void place(int c, int D) {
+    const int k = 8 * c + 8 - D;   // values past the end
+    if (k > 0) {
+      uint64_t lo = a[0] | (uint64_t)a[1] << 32, hi = a[2] | (uint64_t)a[3] << 32;
+      if (k & 4 || k >= 8) {
+        lo = hi;
+        hi = 0;
+      }
+      const int sh = 16 * (k & 3);
+      lo = k >= 8 ? 0 : lo >> sh | hi << 1 << (63 - sh);
+      hi = k >= 8 ? 0 : hi >> sh;
+      a = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    }
+  }
+  __device__ __forceinline__ void unpack(float* v) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[2 * j] = __uint_as_float(a[j] << 16);
       v[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
     }
+  }
+};
+template <>
+struct RawChunk<float> {
+  float f[8];
+  __device__ __forceinline__ void load(const float* row, int c, int D) {
+    const float* p = row + chunk_start(c, D);
+    const u32x4_a4 a = reinterpret_cast<const u32x4_a4*>(p)[0], b = reinterpret_cast<const u32x4_a4*>(p)[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = __uint_as_float(a[j]);
+      f[4 + j] = __uint_as_float(b[j]);
+    }
+  }
+  __device__ __forceinline__ void place(int c, int D) {
+    const int k = 8 * c + 8 - D;   // values past the end
+    if (k > 0) {
+#pragma unroll
+      for (int by = 4; by; by >>= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = k & by ? (j + by < 8 ? f[j + by] : 0.f) : f[j];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = k >= 8 ? 0.f : f[j];
+    }
+  }
+  __device__ __forceinline__ void unpack(float* v) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f[j];
+  }
+};
+
+__device__ __forceinline__ float row_value(const float* row, int64_t i) { return row[i]; }
+__device__ __forceinline__ float row_value(const uint16_t* row, int64_t i) { return bf16_to_f32(row[i]); }
+
+// A chunk loaded and unpacked at once, of rows of any width.
+template <typename T>
+__device__ __forceinline__ void load_chunk(const T* row, int c, int D, float* v) {
+  if (D >= kRowChunkMin) {
+    RawChunk<T> r;
+    r.load(row, c, D);
+    r.place(c, D);
+    r.unpack(v);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 8 * c + j < D ? bf16_to_f32(row[8 * (int64_t)c + j]) : 0.f;
+    for (int j = 0; j < 8; ++j) v[j] = 8 * c + j < D ? row_value(row, 8 * (int64_t)c + j) : 0.f;
   }
 }
 
-// The same eight values stored, rounded once to the row's type (to nearest, ties to even).
+// Eight values stored as chunk c, rounded once to the row's type (to nearest, ties to even).
 __device__ __forceinline__ void store_chunk(float* row, int c, int D, const float* v) {
   if (8 * c + 8 <= D) {
     u32x4_a4 a, b;
@@ -77,42 +130,6 @@ __device__ __forceinline__ void store_chunk(uint16_t* row, int c, int D, const f
       if (8 * c + j < D) row[8 * (int64_t)c + j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
   }
 }
-
-// A chunk as it lies in memory, so that a load can be held in flight and unpacked when it is used.
-template <typename T>
-struct RawChunk;
-template <>
-struct RawChunk<uint16_t> {
-  u32x4 a;
-  __device__ __forceinline__ void load(const uint16_t* row, int c, int D) {
-    if (8 * c + 8 <= D) {
-      a = *reinterpret_cast<const u32x4_a2*>(row + 8 * (int64_t)c);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = 8 * c + 2 * j < D ? row[8 * (int64_t)c + 2 * j] : 0u;
-        const uint32_t hi = 8 * c + 2 * j + 1 < D ? row[8 * (int64_t)c + 2 * j + 1] : 0u;
-        a[j] = lo | hi << 16;
-      }
-    }
-  }
-  __device__ __forceinline__ void unpack(float* v) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(a[j] << 16);
-      v[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
-    }
-  }
-};
-template <>
-struct RawChunk<float> {
-  float f[8];
-  __device__ __forceinline__ void load(const float* row, int c, int D) { load_chunk(row, c, D, f); }
-  __device__ __forceinline__ void unpack(float* v) const {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = f[j];
-  }
-};
 
 // v of the lane that a DPP pattern within 16 lanes names (every lane has a partner in the patterns used
 // here), and the sum of v and that.
@@ -184,8 +201,34 @@ __device__ __forceinline__ T workgroup_sum(T v, T* sh) {
   return s;
 }
 
-// Widest row that a wave holds in registers (64 lanes, four chunks each); wider ones are read once per
-// pass by a workgroup each.
-constexpr int kRowWaveMax = 64 * 4 * 8;
+// Widest row that a wave holds in registers (64 lanes, two chunks each), and a workgroup (16 waves, a chunk
+// per lane); wider ones are read once per pass by a workgroup each.
+constexpr int kRowWaveMax = 64 * 2 * 8;
+constexpr int kRowGroupWaves = 16;
+constexpr int kRowGroupMax = kRowGroupWaves * 64 * 8;
+
+// The waves of a workgroup that holds rows of D values, a chunk per lane.
+__host__ __device__ inline int row_group_waves(int32_t D) { return (D + 511) / 512; }
+
+// A barrier for what the waves exchange through LDS alone: loads from memory stay in flight across it (a
+// whole __syncthreads waits for them).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// The first half of a sum over a workgroup of up to kRowGroupWaves waves: each wave's sum to LDS. After the
+// barrier, wave_sums gives every lane the whole, in one fixed order. sh is written again two barriers later.
+template <typename T>
+__device__ __forceinline__ void put_wave_sum(T v, T* sh) {
+  v = group_sum<64>(v);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+}
+template <typename T>
+__device__ __forceinline__ T wave_sums(const T* sh, int waves) {
+  const int l = threadIdx.x & 15;
+  return group_sum<16>(l < waves ? sh[l] : (T)0);
+}
 
 }  // namespace pg

@@ -81,7 +81,7 @@ def check_forward(x, w, b, mask, eps, dtype_y):
 
 
 @pytest.mark.parametrize("D", [1, 2, 7, 8, 31, 64, 100, 128, 129, 255, 256, 257, 511, 512, 1001, 1024, 1025, 2047, 2048,
-                               2049, 4100, 9001])
+                               2049, 2560, 4100, 8192, 8193, 9001])
 @pytest.mark.parametrize("tx,ty", [(BF, BF), (F, F), (F, BF), (BF, F)])
 def test_forward_widths_and_types(D, tx, ty):
     x, w, b = states(5, D, tx, D)
@@ -164,7 +164,7 @@ def gradients(T, D, dtype, seed):
     return torch.randn((T, D), generator=torch.Generator().manual_seed(seed + 77)).to(dtype) / 64
 
 
-@pytest.mark.parametrize("D", [1, 2, 7, 8, 31, 64, 129, 255, 257, 512, 1001, 1024, 2047, 2048, 2049, 4100])
+@pytest.mark.parametrize("D", [1, 2, 7, 8, 31, 64, 129, 255, 257, 512, 1001, 1024, 2047, 2048, 2049, 2560, 4100, 8192, 8193])
 @pytest.mark.parametrize("tx,ty,tdx", [(BF, F, F), (BF, BF, BF), (F, F, BF), (F, BF, F)])
 def test_backward_widths_and_types(D, tx, ty, tdx):
     x, w, _ = states(6, D, tx, D)
