@@ -58,65 +58,172 @@ __device__ __forceinline__ f32x16 mfma_mx4(const i32x4& a, int sa, const i32x4& 
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(aa, bb, c, 4, 4, 0, sa, 0, sb);
 }
 
-// Any width: the wave's 32 rows and each block of 32 vocabulary rows meet step by step, both read from
-// memory. Lane l holds row l % 32 of either side, the step's half l / 32, and its block's scale.
-__global__ __launch_bounds__(256) void fwd_mx4_stream_kernel(FwdMx4Params p) {
+// The scale bytes of a lane's half of each step: of 16 bytes (blocks 0 .. 15) bytes h, h + 2, ...: byte j
+// of word i belongs to step 4 i + j.
+template <int NW>
+__device__ __forceinline__ void mx4_lane_scales(const i32x4* row, int h, int (&out)[NW]) {
+  const uint32_t sel = h ? 0x07050301u : 0x06040200u;
+#pragma unroll
+  for (int i = 0; i < NW; ++i)
+    out[i] = (int)__builtin_amdgcn_perm((uint32_t)row[i >> 1][2 * (i & 1) + 1], (uint32_t)row[i >> 1][2 * (i & 1)], sel);
+}
+
+template <int OP>
+__device__ __forceinline__ f32x16 mfma_mx4_op(const i32x4& a, int sa, const i32x4& b, int sb, const f32x16& c) {
+  const i32x8 aa = {a[0], a[1], a[2], a[3]}, bb = {b[0], b[1], b[2], b[3]};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(aa, bb, c, 4, 4, OP, sa, OP, sb);
+}
+
+// Step k of a chain (an unrolled loop's k is a constant, which the switch folds on): words of four steps'
+// scales, byte k % 4.
+__device__ __forceinline__ f32x16 mx4_step(int k, const i32x4& a, const int* sa, const i32x4& b, const int* sb,
+                                           const f32x16& acc) {
+  switch (k & 3) {
+    case 0: return mfma_mx4_op<0>(a, sa[k >> 2], b, sb[k >> 2], acc);
+    case 1: return mfma_mx4_op<1>(a, sa[k >> 2], b, sb[k >> 2], acc);
+    case 2: return mfma_mx4_op<2>(a, sa[k >> 2], b, sb[k >> 2], acc);
+    default: return mfma_mx4_op<3>(a, sa[k >> 2], b, sb[k >> 2], acc);
+  }
+}
+
+// Any width: a wave holds the sums of 64 rows against 64 vocabulary rows (four accumulators, so that each
+// fragment is used twice) and both sides' fragments come from memory, two steps ahead of their use. Lane l
+// holds row l % 32 of a fragment, the step's half l / 32, and its block's scale.
+constexpr int kMx4StreamRows = 256, kMx4StreamTile = 64;
+struct Mx4Fragments {
+  i32x4 a[2], b[2];   // of the vocabulary, of the states
+};
+
+__global__ __launch_bounds__(256, 2) void fwd_mx4_stream_kernel(FwdMx4Params p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, col = lane & 31;
   const int64_t n = p.n_dev ? (int64_t)(*p.n_dev) : p.n_host;
-  const int S = mx4_splits(p, n, p.nblocks);
+  const int ntiles = (p.V + kMx4StreamTile - 1) / kMx4StreamTile, steps = p.steps;
+  const int S = mx4_splits(p, n, ntiles);
   const int64_t rt = blockIdx.x / S;
   const int split = blockIdx.x % S;
-  const int64_t tok0 = rt * 128 + wave * 32;
+  const int64_t tok0 = rt * kMx4StreamRows + wave * 64;
   if (tok0 >= n) return;
-  const int per = (p.nblocks + S - 1) / S;
-  const int b0 = split * per, b1 = min(b0 + per, p.nblocks);
+  const int per = (ntiles + S - 1) / S;
+  const int b0 = split * per, b1 = min(b0 + per, ntiles);
 
-  const int64_t tok = tok0 + col;
-  const int64_t ic = tok < n ? tok : n - 1;
-  const int64_t row = p.rows ? (int64_t)p.rows[ic] : ic;
-  const uint8_t* hc = p.hc + row * p.cb + 16 * h;
-  const uint8_t* hs = p.hs + row * p.sb + h;
-  const int y = p.target[row];
-  float m = -INFINITY, l = 0.f, sy = -INFINITY;
+  constexpr int kAhead = 2;
+  const uint8_t *hc[2], *hs[2];
+  int y[2];
+  float m[2], l[2], sy[2];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int64_t tok = tok0 + 32 * g + col;
+    const int64_t ic = tok < n ? tok : n - 1;
+    const int64_t row = p.rows ? (int64_t)p.rows[ic] : ic;
+    hc[g] = p.hc + row * p.cb + 16 * h;
+    hs[g] = p.hs + row * p.sb;
+    y[g] = p.target[row];
+    m[g] = sy[g] = -INFINITY;
+    l[g] = 0.f;
+  }
   for (int b = b0; b < b1; ++b) {
-    const int64_t v = min(b * 32 + col, p.V - 1);
-    const uint8_t* ec = p.ec + v * p.cb + 16 * h;
-    const uint8_t* es = p.es + v * p.sb + h;
-    f32x16 acc = {};
-    for (int k = 0; k < p.steps; ++k)
-      acc = mfma_mx4(*reinterpret_cast<const i32x4*>(ec + 32 * k), es[2 * k], *reinterpret_cast<const i32x4*>(hc + 32 * k),
-                     hs[2 * k], acc);
-    // register r: vocabulary row 8 (r / 4) + 4 h + r % 4 of the block
-    float s2[16], bm = -INFINITY;
+    const uint8_t *ec[2], *es[2];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int vr = b * 32 + 8 * (r >> 2) + 4 * h + (r & 3);
-      s2[r] = vr < p.V ? capped_log2(acc[r], p.sc) : -INFINITY;
-      bm = fmaxf(bm, s2[r]);
-      if (vr == y && vr < p.V) sy = s2[r];
+    for (int i = 0; i < 2; ++i) {
+      const int64_t v = min(b * kMx4StreamTile + 32 * i + col, p.V - 1);
+      ec[i] = p.ec + v * p.cb + 16 * h;
+      es[i] = p.es + v * p.sb;
     }
-    const float mn = fmaxf(m, bm);
-    if (mn != -INFINITY) {
+    f32x16 acc[2][2] = {};
+    Mx4Fragments f[2][kAhead];
+    int sa[2][2], sb[2][2];
+    // the kAhead steps from k on (past the end: the last one, which is not used)
+    auto load = [&](Mx4Fragments (&to)[kAhead], int k) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int64_t at = 32 * (int64_t)min(k + j, steps - 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          to[j].a[i] = *reinterpret_cast<const i32x4*>(ec[i] + at);
+          to[j].b[i] = *reinterpret_cast<const i32x4*>(hc[i] + at);
+        }
+      }
+    };
+    // scales of steps k .. k + 7 (a row's scales are padded to 16 bytes)
+    auto scales = [&](int k) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mx4_lane_scales(reinterpret_cast<const i32x4*>(es[i] + 2 * k), h, sa[i]);
+        mx4_lane_scales(reinterpret_cast<const i32x4*>(hs[i] + 2 * k), h, sb[i]);
+      }
+    };
+    auto step = [&](const Mx4Fragments& f, int j) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) acc[i][g] = mx4_step(j, f.a[i], sa[i], f.b[g], sb[g], acc[i][g]);
+    };
+    load(f[0], 0);
+    int k = 0;
+    for (; k + 8 <= steps; k += 8) {
+      scales(k);
+#pragma unroll
+      for (int q = 0; q < 8 / kAhead; ++q) {
+        load(f[(q + 1) & 1], k + kAhead * (q + 1));
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) step(f[q & 1][j], kAhead * q + j);
+      }
+    }
+    if (k < steps) {
+      scales(k);
+#pragma unroll
+      for (int q = 0; q < 8 / kAhead; ++q) {
+        load(f[(q + 1) & 1], k + kAhead * (q + 1));
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (k + kAhead * q + j < steps) step(f[q & 1][j], kAhead * q + j);
+      }
+    }
+    // register r: vocabulary row 8 (r / 4) + 4 h + r % 4 of the block
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      float s2[2][16], bm = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int vr = b * kMx4StreamTile + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
+          s2[i][r] = vr < p.V ? capped_log2(acc[i][g][r], p.sc) : -INFINITY;
+          bm = fmaxf(bm, s2[i][r]);
+          if (vr == y[g] && vr < p.V) sy[g] = s2[i][r];
+        }
+      const float mn = fmaxf(m[g], bm);
       float part = 0.f;
+      if (mn != -INFINITY) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) part += fexp2(s2[r] - mn);
-      l = l * fexp2(m - mn) + part;
-      m = mn;
-    } else {
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) l += s2[r] != s2[r] ? s2[r] : 0.f;   // NaN rows stay NaN
+          for (int r = 0; r < 16; ++r) part += fexp2(s2[i][r] - mn);
+        l[g] = l[g] * fexp2(m[g] - mn) + part;
+        m[g] = mn;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) l[g] += s2[i][r] != s2[i][r] ? s2[i][r] : 0.f;   // NaN rows stay NaN
+      }
     }
   }
-  lse_merge(m, l, __shfl_xor(m, 32), __shfl_xor(l, 32));
-  const float sy2 = __shfl_xor(sy, 32);
-  const bool here = y >= b0 * 32 && y < b1 * 32 && y < p.V;   // this split holds the target's row
-  if (h == 0 && tok < n) {
-    const int64_t at = tok * mx4_split_stride(S) + split;
-    p.part_l[at] = l;
-    p.part_m[at] = m;
-    if (here) p.s_target[tok] = ((y >> 2) & 1) ? sy2 : sy;
-    else if (split == 0 && !(y >= 0 && y < p.V)) p.s_target[tok] = __builtin_nanf("");
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int64_t tok = tok0 + 32 * g + col;
+    lse_merge(m[g], l[g], __shfl_xor(m[g], 32), __shfl_xor(l[g], 32));
+    const float sy2 = __shfl_xor(sy[g], 32);
+    // this split holds the target's row
+    const bool here = y[g] >= b0 * kMx4StreamTile && y[g] < b1 * kMx4StreamTile && y[g] < p.V;
+    if (h == 0 && tok < n) {
+      const int64_t at = tok * mx4_split_stride(S) + split;
+      p.part_l[at] = l[g];
+      p.part_m[at] = m[g];
+      if (here) p.s_target[tok] = ((y[g] >> 2) & 1) ? sy2 : sy[g];
+      else if (split == 0 && !(y[g] >= 0 && y[g] < p.V)) p.s_target[tok] = __builtin_nanf("");
+    }
   }
 }
 
@@ -172,34 +279,6 @@ __device__ __forceinline__ void lds_dma4_base(const uint8_t* base, uint32_t offs
       : "=&s"(saved)
       : "v"(offset), "s"(base), "s"(lds_addr)
       : "memory");
-}
-
-// The scale bytes of a lane's half of each step: of 16 bytes (blocks 0 .. 15) bytes h, h + 2, ...: byte j
-// of word i belongs to step 4 i + j.
-template <int NW>
-__device__ __forceinline__ void mx4_lane_scales(const i32x4* row, int h, int (&out)[NW]) {
-  const uint32_t sel = h ? 0x07050301u : 0x06040200u;
-#pragma unroll
-  for (int i = 0; i < NW; ++i)
-    out[i] = (int)__builtin_amdgcn_perm((uint32_t)row[i >> 1][2 * (i & 1) + 1], (uint32_t)row[i >> 1][2 * (i & 1)], sel);
-}
-
-template <int OP>
-__device__ __forceinline__ f32x16 mfma_mx4_op(const i32x4& a, int sa, const i32x4& b, int sb, const f32x16& c) {
-  const i32x8 aa = {a[0], a[1], a[2], a[3]}, bb = {b[0], b[1], b[2], b[3]};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(aa, bb, c, 4, 4, OP, sa, OP, sb);
-}
-
-// Step k of a chain (an unrolled loop's k is a constant, which the switch folds on): words of four steps'
-// scales, byte k % 4.
-__device__ __forceinline__ f32x16 mx4_step(int k, const i32x4& a, const int* sa, const i32x4& b, const int* sb,
-                                           const f32x16& acc) {
-  switch (k & 3) {
-    case 0: return mfma_mx4_op<0>(a, sa[k >> 2], b, sb[k >> 2], acc);
-    case 1: return mfma_mx4_op<1>(a, sa[k >> 2], b, sb[k >> 2], acc);
-    case 2: return mfma_mx4_op<2>(a, sa[k >> 2], b, sb[k >> 2], acc);
-    default: return mfma_mx4_op<3>(a, sa[k >> 2], b, sb[k >> 2], acc);
-  }
 }
 
 // Forms of the sum: a softcap in the fixed-shift range, no softcap, a larger softcap (the last two with a
@@ -634,10 +713,10 @@ hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const u
     p.rows = reinterpret_cast<const int32_t*>(ws + L.rows);
     p.n_dev = reinterpret_cast<const int32_t*>(ws + L.n_rows);
   }
-  // the partial sums' room: splits x rows stays within grid x 128, and the workspace holds
-  // max(ceil(T / 256), 1024) x 256 of them
+  // the partial sums' room: splits x rows stays within 1024 x 128 where there are splits, and the
+  // workspace holds max(ceil(T / 256), 1024) x 256 of them
   const int ncu = dev.cu_count > 0 ? dev.cu_count : 256;
-  int tile = 32, fixed = 0, direct = 0;
+  int tile = 0, fixed = 0, direct = 0;
   p.rows_per_wg = 128;
   if (p.steps <= 16) {
     const bool wide = p.steps <= 8 && !mask && T >= (int64_t)256 * ncu;
@@ -689,8 +768,10 @@ hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const u
       default: launch_fwd_mx4_ks<16>(p, st); break;
     }
   } else {
-    const int64_t rt = (T + 127) / 128;
-    p.aim = 1024;
+    p.rows_per_wg = kMx4StreamRows;
+    tile = kMx4StreamTile;
+    const int64_t rt = (T + kMx4StreamRows - 1) / kMx4StreamRows;
+    p.aim = 512;
     p.grid = (int)(rt > p.aim ? rt : p.aim);
     hipLaunchKernelGGL(fwd_mx4_stream_kernel, dim3(p.grid), dim3(256), 0, st, p);
   }
