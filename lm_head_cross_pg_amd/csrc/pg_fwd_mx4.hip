@@ -533,7 +533,7 @@ __global__ __launch_bounds__(512, KS <= 8 && RB == 1 ? 4 : 2) void fwd_mx4_kerne
     for (int rb = 0; rb < RB; ++rb)
       add(rb, prev[rb], (tw - 1) * TL::kRows + (TL::kBlocksPerWave - 1) * 64 + half * 32);
   }
-  if (tw < t1) {
+  if (t0 <= tw && tw < t1) {   // (a split without tiles starts past the last one)
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __syncthreads();                             // nothing is in flight to buffer 0, and no one reads it
     load_last(tw, 0);

@@ -205,6 +205,17 @@ def test_head_widths(D, c, gain):
     check_head(70, D, 333, c, D, gain)
 
 
+@pytest.mark.parametrize("scored", [130, 300, 900, 1500, 2000])
+@pytest.mark.parametrize("D,V", [(200, 5003), (640, 5003), (1100, 5003), (64, 1291)])
+@pytest.mark.parametrize("c", [30.0, 0.0])
+def test_head_splits_without_tiles(scored, D, V, c):
+    """Splits of the vocabulary whose share of tiles is empty (40 tiles over 21 splits are 20 splits of two and
+    one of none) next to a last tile that is not whole: every row of the vocabulary counts once."""
+    T = scored + 70
+    mask = (torch.arange(T) >= 70).to(torch.uint8)
+    check_head(T, D, V, c, scored, mask=mask, sample=np.arange(60, T, 37))
+
+
 @pytest.mark.parametrize("V", [1, 2, 31, 32, 33, 63, 64, 65, 127, 129, 1000, 8192, 8193])
 @pytest.mark.parametrize("c", [30.0, 0.0])
 def test_head_vocabularies(V, c):
