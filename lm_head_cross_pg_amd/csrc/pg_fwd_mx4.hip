@@ -2,6 +2,11 @@
 // microscaled 4-bit format (pg_mx4.h), their product by v_mfma_scale_f32_32x32x64_f8f6f4 (every value
 // of both formats and every product of two is exact; the sum over D is float32), then the softcap,
 // log-sum-exp and cross-entropy of the bf16 forward without the T x V logits ever reaching memory.
+//
+// Bound: an fp4 product of 512 deep is done in half the time that softcap and exponential of its logits
+// take, so the vector units set the pace: 98 instructions per 32 x 32 logits (of them two transcendentals per
+// logit), 96 at least. 65536 x 512 x 8192 takes 180 us (3.05 PFLOP/s; the bf16 forward 440), of which vector
+// instructions issue for 81 %, at 2.2 GHz (constant inputs, which draw less power: 10 % less).
 #include "pg_internal.h"
 #include "pg_mx4.h"
 
@@ -88,7 +93,9 @@ __device__ __forceinline__ f32x16 mx4_step(int k, const i32x4& a, const int* sa,
 
 // Any width: a wave holds the sums of 64 rows against 64 vocabulary rows (four accumulators, so that each
 // fragment is used twice) and both sides' fragments come from memory, two steps ahead of their use. Lane l
-// holds row l % 32 of a fragment, the step's half l / 32, and its block's scale.
+// holds row l % 32 of a fragment, the step's half l / 32, and its block's scale. Bound by the first-level
+// cache, where a fragment's 32 rows are 32 lines: 4096 x 2048 x 8192 in 158 us (0.9 PFLOP/s; 32 x 32 logits a
+// wave without loads ahead 457; four steps ahead do not fit the registers).
 constexpr int kMx4StreamRows = 256, kMx4StreamTile = 64;
 struct Mx4Fragments {
   i32x4 a[2], b[2];   // of the vocabulary, of the states
@@ -233,7 +240,9 @@ __global__ __launch_bounds__(256, 2) void fwd_mx4_stream_kernel(FwdMx4Params p) 
 // registers (the B operand) and take the even and the odd 32-row blocks of each vocabulary tile. The
 // tiles stream through LDS, two buffers, copied there by DMA while the tile before is worked on; every
 // wave reads the fragments of its blocks from LDS (the A operand). An accumulator holds 16 vocabulary
-// rows of one token per lane, so the softcap and the sum of exponentials run per lane.
+// rows of one token per lane, so the softcap and the sum of exponentials run per lane. Where there
+// are 256 rows for every CU, a wave holds 64 of them (RB = 2): each fragment read then feeds two products (65536
+// rows: 199 -> 188 us); with fewer rows 32 a wave make more workgroups.
 template <int KS>
 struct Mx4Tile {
   static constexpr int kRows = KS <= 8 ? 128 : 64;                // vocabulary rows of a tile

@@ -104,7 +104,7 @@ hipError_t launch_norm_mx4(const void* x, int32_t dtype_x, const float* weight, 
                            const DeviceInfo& dev, hipStream_t st);
 struct NormBwdWorkspace {
   size_t part;    // f32[blocks, 2, D]: partial sums of the gradients of the gain and the bias
-  size_t stats;   // f64[T, 2]: mean and reciprocal deviation of each row (rows wider than a wave holds)
+  size_t stats;   // f64[T, 2]: mean and reciprocal deviation of each row (rows that no lanes hold)
   size_t total;
 };
 NormBwdWorkspace norm_bwd_workspace(int64_t T, int32_t D);

@@ -2,7 +2,9 @@
 // tied embedding and the states that meet it in the 4-bit head, and the fake quantisation of
 // quantisation-aware training (trios issue #19, approach table, "Квантование": INT4/INT8; README
 // leaderboard, QAT rows). Both are one pass over the data, bound by HBM: a lane holds eight values, four lanes a
-// block of 32, so that a block's largest magnitude takes two lane exchanges.
+// block of 32, so that a block's largest magnitude takes two lane exchanges. 32768 x 1024 float32 values take
+// 25 us (6.2 TB/s read and written) to 4 bits and 27 back; 65536 x 512 bf16 ones 16 (5.2) and 15 (5.7 TB/s; 21
+// with the levels formed by integer arithmetic instead of the hardware's conversion).
 #include "pg_internal.h"
 #include "pg_mx4.h"
 #include "pg_rows.h"
