@@ -21,13 +21,13 @@ struct FwdMx4Params {
   const uint8_t* ec;
   const uint8_t* es;
   const int32_t* target;
-  const int32_t* rows;    // compacted scored rows, or nullptr (row i = i)
-  const int32_t* n_dev;   // device row count, or nullptr (use n_host)
+  const uint8_t* mask;    // rows to select in the kernel itself, or nullptr
+  int32_t* rows;          // compacted scored rows, or nullptr (row i = i)
+  int32_t* n_dev;         // device row count, or nullptr (use n_host)
   int64_t n_host;
   int64_t cb, sb;         // bytes of a row of codes, of scales
   int steps;              // 64-value steps of a row
   int V;
-  int nblocks;            // 32-row blocks of the vocabulary
   int grid;               // workgroups of the launch
   int aim;                // workgroups that splits make of few rows
   int rows_per_wg;
@@ -290,6 +290,98 @@ __device__ __forceinline__ void lds_dma4_base(const uint8_t* base, uint32_t offs
       : "memory");
 }
 
+// Selection of the scored rows by the head itself, for 16 to kMx4MaskRows rows: every workgroup reads the whole
+// mask (from L2, at most 64 KiB), counts, and keeps its own 128 rows in LDS, which takes 5 us at 65536 rows and 3
+// at 3001. A launch of its own for the list takes 7 and 4 and the gap between two launches (the call with 2048
+// of 65536 rows scored: 22.9 -> 21.4 us; with half of 3001: 16.8 -> 14.7).
+constexpr int kMx4MaskPiece = 1024;                        // rows that a wave takes at once, 16 a lane
+constexpr int kMx4MaskPieces = 8;                          // pieces of a wave, at most
+constexpr int kMx4MaskRows = 8 * kMx4MaskPieces * kMx4MaskPiece;
+// The sum of v over this lane and those below: within runs of 16 lanes, then the runs before.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast 15, 31
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+  return v;
+}
+struct Mx4MaskRows {
+  uint32_t bits[kMx4MaskPieces];   // of this lane's 16 rows in each piece
+  int before[kMx4MaskPieces];      // scored rows of the piece in lower lanes
+  int total[kMx4MaskPieces];       // of the piece (uniform)
+  int base;                        // in lower waves (uniform)
+  int pieces;                      // of a wave
+
+  __device__ __forceinline__ int row0(int wave, int lane, int q) const {
+    return (wave * pieces + q) * kMx4MaskPiece + 16 * lane;
+  }
+  // Counts; returns the number of scored rows. sums: eight entries of LDS.
+  __device__ __forceinline__ int count(const uint8_t* mask, int T, int wave, int lane, int* sums) {
+    pieces = (T + 8 * kMx4MaskPiece - 1) / (8 * kMx4MaskPiece);
+    typedef uint32_t u32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
+    u32x4_a1 w[kMx4MaskPieces];
+#pragma unroll
+    for (int q = 0; q < kMx4MaskPieces; ++q) {   // (16 rows that the mask's end cuts are read from T - 16 on)
+      w[q] = u32x4_a1{0, 0, 0, 0};
+      if (q < pieces && row0(wave, lane, q) < T)
+        w[q] = *reinterpret_cast<const u32x4_a1*>(mask + min(row0(wave, lane, q), T - 16));
+    }
+    int counts[kMx4MaskPieces / 2];
+#pragma unroll
+    for (int q = 0; q < kMx4MaskPieces; ++q) {
+      uint32_t b = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {   // a bit per nonzero byte
+        const uint32_t f = ((((w[q][k] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w[q][k]) & 0x80808080u) >> 7;
+        b |= ((f * 0x01020408u) >> 24 & 15u) << (4 * k);
+      }
+      bits[q] = b >> min(max(row0(wave, lane, q) + 16 - T, 0), 31);
+      counts[q / 2] = q & 1 ? counts[q / 2] | __popc(bits[q]) << 16 : __popc(bits[q]);
+    }
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < kMx4MaskPieces / 2; ++k) {   // two pieces to a scan (a piece has at most 1024)
+      const int upto = wave_scan(counts[k]), below = upto - counts[k], all = __builtin_amdgcn_readlane(upto, 63);
+      before[2 * k] = below & 0xffff;
+      before[2 * k + 1] = below >> 16;
+      total[2 * k] = all & 0xffff;
+      total[2 * k + 1] = all >> 16;
+      mine += total[2 * k] + total[2 * k + 1];
+    }
+    if (lane == 0) sums[wave] = mine;
+    lds_barrier();
+    int n = 0;
+    base = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int v = sums[k];
+      n += v;
+      base += k < wave ? v : 0;
+    }
+    base = __builtin_amdgcn_readfirstlane(base);
+    return __builtin_amdgcn_readfirstlane(n);
+  }
+  // The scored rows lo .. lo + 127 to list, and to rows + lo where `rows` is given.
+  __device__ __forceinline__ void keep(int lo, int wave, int lane, int* list, int32_t* rows) const {
+    int start = base;
+#pragma unroll
+    for (int q = 0; q < kMx4MaskPieces; ++q) {
+      if (start < lo + 128 && start + total[q] > lo) {
+        int at = start + before[q] - lo;
+        for (uint32_t b = bits[q]; b; b &= b - 1, ++at) {
+          if ((uint32_t)at >= 128u) continue;
+          const int row = row0(wave, lane, q) + __ffs(b) - 1;
+          list[at] = row;
+          if (rows) rows[lo + at] = row;
+        }
+      }
+      start += total[q];
+    }
+  }
+};
+
 // Forms of the sum: a softcap in the fixed-shift range, no softcap, a larger softcap (the last two with a
 // reference that follows the largest logit).
 enum Mx4Form { kMx4Fixed, kMx4Uncapped, kMx4Capped };
@@ -302,11 +394,21 @@ __global__ __launch_bounds__(512, KS <= 8 && RB == 1 ? 4 : 2) void fwd_mx4_kerne
   constexpr int NS = TL::kScaleBytes / 16;
   __shared__ __attribute__((aligned(1024))) char smem[2 * TL::kBytes];
   __shared__ float merge[2][RB][4][32];
+  __shared__ int list[128], sums[8];
   const lds_char* lds = (const lds_char*)smem;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, col = lane & 31;
-  const int64_t n = p.n_dev ? (int64_t)(*p.n_dev) : p.n_host;
+  Mx4MaskRows own;
+  int64_t n;
+  const bool select = RB == 1 && p.mask != nullptr;
+  if (select) {
+    const int T = (int)p.n_host;
+    n = own.count(p.mask, T, wave, lane, sums);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.n_dev = (int)n;
+  } else {
+    n = p.n_dev ? (int64_t)(*p.n_dev) : p.n_host;
+  }
   const int ntiles = (p.V + TL::kRows - 1) / TL::kRows;
   // the host's choice comes as a grid of splits x row tiles (row tiles alone for one split): no divisions
   int S = p.splits, per = p.per, split = 0;
@@ -321,6 +423,10 @@ __global__ __launch_bounds__(512, KS <= 8 && RB == 1 ? 4 : 2) void fwd_mx4_kerne
     split = blockIdx.x;
   }
   if (rt * (128 * RB) >= n) return;
+  if (select) {
+    own.keep((int)rt * 128, wave, lane, list, split == 0 ? p.rows : nullptr);
+    lds_barrier();
+  }
   const int t0 = split * per, t1 = min(t0 + per, ntiles);
 
   // This wave's part of a tile: kLoads pieces of codes (piece j: 1 KiB, lane i its 16 bytes at 16 i), and
@@ -363,16 +469,17 @@ __global__ __launch_bounds__(512, KS <= 8 && RB == 1 ? 4 : 2) void fwd_mx4_kerne
 
   // the rows of this wave: codes and scales
   const int rg = wave & 3, half = wave >> 2;
-  auto token = [&](int rb) { return rt * (128 * RB) + (rg * RB + rb) * 32 + col; };
-  auto row_of = [&](int rb) {
-    const int64_t tok = token(rb), i = tok < n ? tok : n - 1;
+  auto token = [&](int rb, int c) { return rt * (128 * RB) + (rg * RB + rb) * 32 + c; };
+  auto row_of = [&](int rb, int c) {
+    if (select) return (int64_t)list[min((rg * RB + rb) * 32 + c, (int)(n - rt * 128) - 1)];
+    const int64_t tok = token(rb, c), i = tok < n ? tok : n - 1;
     return p.rows ? (int64_t)p.rows[i] : i;
   };
   i32x4 hf[RB][KS];
   int hs[RB][NW];
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
-    const int64_t row = row_of(rb);
+    const int64_t row = row_of(rb, col);
     const i32x4* src = reinterpret_cast<const i32x4*>(p.hc + row * p.cb + 16 * h);
 #pragma unroll
     for (int k = 0; k < KS; ++k) hf[rb][k] = k < p.steps ? src[2 * k] : i32x4{};
@@ -580,11 +687,13 @@ __global__ __launch_bounds__(512, KS <= 8 && RB == 1 ? 4 : 2) void fwd_mx4_kerne
   }
   __syncthreads();
   if (half == 1) return;
+  int c = col;   // not seen through, so that nothing formed from it is kept in registers over the loop above
+  asm volatile("" : "+v"(c));
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
     if constexpr (FIXED) l[rb] += merge[1][rb][rg][col];
     else lse_merge(m[rb], l[rb], merge[0][rb][rg][col], merge[1][rb][rg][col]);
-    const int64_t tok = token(rb), row = row_of(rb);
+    const int64_t tok = token(rb, c), row = row_of(rb, c);
 
     // The targets' logits: the 32 target rows as the A operand, whose product with the 32 tokens has them
     // on the diagonal, formed by the same instructions from the same values as the sum's.
@@ -636,6 +745,13 @@ constexpr int kMx4FinalLanes = 16, kMx4FinalRows = 256 / kMx4FinalLanes;
 __global__ __launch_bounds__(256) void fwd_mx4_finalize_kernel(FwdMx4Params p, int tile, int fixed, int direct) {
   const int64_t n = p.n_dev ? (int64_t)(*p.n_dev) : p.n_host;
   const int S = mx4_splits(p, n, (p.V + tile - 1) / tile);
+  if (p.mask) {   // rows that are left out
+    for (int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < p.n_host; r += (int64_t)gridDim.x * blockDim.x) {
+      if (p.mask[r]) continue;
+      p.nats[r] = 0.f;
+      if (p.lse) p.lse[r] = 0.f;
+    }
+  }
   if (direct && S == 1) return;
   const int stride = mx4_split_stride(S), lane = threadIdx.x % kMx4FinalLanes;
   for (int64_t i = (int64_t)blockIdx.x * kMx4FinalRows + threadIdx.x / kMx4FinalLanes; i < n;
@@ -709,7 +825,6 @@ hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const u
   p.sb = mx4_scale_bytes(D);
   p.steps = (D + kMx4Step - 1) / kMx4Step;
   p.V = V;
-  p.nblocks = (V + 31) / 32;
   p.sc = Softcap::make(cap);
   p.nats = nats;
   p.lse = lse;
@@ -717,10 +832,14 @@ hipError_t launch_fwd_mx4(const uint8_t* hcodes, const uint8_t* hscales, const u
   p.part_m = reinterpret_cast<float*>(ws + L.part_m);
   p.s_target = reinterpret_cast<float*>(ws + L.s_target);
   if (mask) {
-    hipError_t e = launch_compact_rows(mask, T, ws, L, nats, lse, st);
-    if (e != hipSuccess) return e;
-    p.rows = reinterpret_cast<const int32_t*>(ws + L.rows);
-    p.n_dev = reinterpret_cast<const int32_t*>(ws + L.n_rows);
+    p.rows = reinterpret_cast<int32_t*>(ws + L.rows);
+    p.n_dev = reinterpret_cast<int32_t*>(ws + L.n_rows);
+    if (p.steps <= 16 && T >= 16 && T <= kMx4MaskRows) {
+      p.mask = mask;
+    } else {
+      hipError_t e = launch_compact_rows(mask, T, ws, L, nats, lse, st);
+      if (e != hipSuccess) return e;
+    }
   }
   // the partial sums' room: splits x rows stays within 1024 x 128 where there are splits, and the
   // workspace holds max(ceil(T / 256), 1024) x 256 of them

@@ -205,6 +205,18 @@ def test_head_widths(D, c, gain):
     check_head(70, D, 333, c, D, gain)
 
 
+@pytest.mark.parametrize("T", [1, 15, 16, 17, 129, 1023, 1040, 8191, 8192, 8193, 16385, 65535, 65536, 65537])
+@pytest.mark.parametrize("part", [0.02, 0.5, 1.0])
+def test_head_selects_scored_rows(T, part):
+    """Every count of rows that a wave, a piece of the mask and a workgroup end in, any nonzero byte scoring."""
+    g = torch.Generator().manual_seed(T)
+    value = torch.tensor([1, 2, 128, 255], dtype=torch.uint8)[torch.randint(0, 4, (T,), generator=g)]
+    mask = torch.where(torch.rand(T, generator=g) < part, value, torch.zeros_like(value))
+    at = np.unique(np.concatenate([np.arange(min(T, 40)), np.arange(max(0, T - 40), T),
+                                   torch.randint(0, T, (200,), generator=g).numpy()]))
+    check_head(T, 33, 70, 30.0, T, mask=mask, sample=at)
+
+
 @pytest.mark.parametrize("scored", [130, 300, 900, 1500, 2000])
 @pytest.mark.parametrize("D,V", [(200, 5003), (640, 5003), (1100, 5003), (64, 1291)])
 @pytest.mark.parametrize("c", [30.0, 0.0])
