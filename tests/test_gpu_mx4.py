@@ -433,3 +433,38 @@ def test_head_widest_vocabulary_and_states():
     check_head(5, 1 << 16, 70, 30.0, 51)
     mask = torch.tensor([1, 0, 1, 1, 0], dtype=torch.uint8)
     check_head(5, 64, 1 << 18, 0.0, 52, mask=mask)
+
+
+def test_captured_head_follows_its_mask():
+    """A captured masked call replayed after the mask's bytes have changed: the rows that it scores now, and as
+    many splits as their number makes."""
+    T, D, V = 5000, 96, 1500
+    hq, eq, y, H, E = head_inputs(T, D, V, 60, 4.0)
+    y = y.cuda()
+    nats, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    ws = torch.empty(abi.workspace_bytes(abi.PG_OP_FWD_MX4, T, D, V), dtype=torch.uint8, device="cuda")
+    mask = torch.ones(T, dtype=torch.uint8, device="cuda")
+
+    def call():
+        abi.pg_lmhead_ce_fwd_mx4(*hq, *eq, y, mask, D, 30.0, nats, lse, ws)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    g = torch.Generator().manual_seed(61)
+    for part in (1.0, 0.5, 0.0, 0.01, 0.9):
+        m = (torch.rand(T, generator=g) < part).to(torch.uint8)
+        mask.copy_(m)
+        nats.fill_(-1.0)
+        lse.fill_(-1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = nats.clone(), lse.clone()
+        call()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], nats) and torch.equal(got[1], lse)
+        on, ol = ora.forward(H, E, y.cpu().numpy(), 30.0, m.numpy())
+        tol = tolerance(H, E, 30.0, V)
+        assert np.max(np.abs(f64(nats) - on)) <= tol and np.max(np.abs(f64(lse) - ol)) <= tol
